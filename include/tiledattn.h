@@ -181,6 +181,87 @@ ta_status attn_lse_merge(float *acc_o, float *acc_lse, const void *part_o, const
 ta_status attn_lse_merge_finish(const float *acc_o, void *out, int64_t rows, int d, ta_stream_t stream);
 
 /*
+ * attn_rope - rotary position embedding of one tensor, or its gradient.
+ * (The source pages take Q and K as given; this call and attn_paged_append
+ * prepare them.)  A row of d elements holds rotary_dim / 2 pairs (a, b):
+ * element i with element i + rotary_dim / 2 (interleaved = 0), or elements
+ * 2i and 2i + 1 (interleaved = 1).  Pair i of a token at position p turns by
+ * t = p * inv_freq[i] radians:
+ *     a' = amplitude (a cos t - b sin t),  b' = amplitude (a sin t + b cos t)
+ * and elements from rotary_dim on are copied.  inverse = 1 turns by -t: with
+ * the same amplitude that is the gradient of the forward call (the transposed
+ * map).  Angles are formed in fp64 and each result is rounded once.
+ *
+ *   x, y         bf16 [B, H, N, d] with the strides given (in elements, for
+ *                batch, head and token; the d elements of a row are
+ *                contiguous): multiples of 8, bases 16-byte aligned.  So x can
+ *                be the heads of a fused projection's [B, N, heads, d] rows
+ *                and y the [B, H, N, d] array attn_fwd reads, or the reverse
+ *                for a gradient.  y may be x itself with the same strides
+ *                (each element is read before it is written); otherwise they
+ *                must not overlap.  Rows of y must be distinct.
+ *   positions    int32, element b * pos_stride_b + n for token n of batch b
+ *                (pos_stride_b = 0: one row for all batches); may be
+ *                negative.  NULL: position n.
+ *   inv_freq     [rotary_dim / 2] fp64, radians per position (any scaling for
+ *                long contexts is in these and the amplitude).  May be NULL if
+ *                rotary_dim is 0 (then the call only copies).
+ *
+ * Supported: d in {64, 128}, rotary_dim a multiple of 16 in [0, d], B * N <
+ * 2^31, H <= 65535, amplitude finite.  B * H * N == 0 does nothing.
+ */
+ta_status attn_rope(const void *x, void *y, const int32_t *positions, const double *inv_freq, int B, int H, int N,
+                    int d, int rotary_dim, int interleaved, int inverse, float amplitude, int64_t x_stride_b,
+                    int64_t x_stride_h, int64_t x_stride_n, int64_t y_stride_b, int64_t y_stride_h,
+                    int64_t y_stride_n, int64_t pos_stride_b, ta_stream_t stream);
+
+/*
+ * attn_paged_append - new tokens into the paged cache, with the rotation of
+ * attn_rope applied on the way: K rows are rotated and written to their page
+ * slots, V rows are written as they are, and (if q is given) Q rows are
+ * rotated into the packed array that attn_paged_prefill and attn_paged_decode
+ * read.
+ *
+ *   q            [total, Hq,  d] bf16 rows with the strides given, or NULL
+ *   k, v         [total, Hkv, d] bf16 rows with the strides given (elements,
+ *                for token and head; multiples of 8), e.g. heads of a fused
+ *                projection's rows
+ *   q_out        [total, Hq, d] bf16, contiguous (required if q is given).
+ *                May be q itself if that is contiguous; must not overlap
+ *                anything else
+ *   cu_seqlens   [num_seqs + 1] int32 as in attn_paged_prefill: sequence s
+ *                brings rows [cu_seqlens[s], cu_seqlens[s+1]), possibly none.
+ *                NULL: one token per sequence (total == num_seqs)
+ *   seq_lens     [num_seqs] int32, the keys of each sequence AFTER the append
+ *                (what the attention calls then take): the last new token goes
+ *                to slot seq_lens[s] - 1.  With cu_seqlens NULL a length of 0
+ *                marks an empty place of the batch: nothing is written for it
+ *   positions    [total] int32 rotation positions; NULL: the token's slot in
+ *                its sequence
+ *   k_cache, v_cache, block_table: as attn_paged_decode (written here)
+ *   inv_freq, rotary_dim, interleaved, amplitude: as attn_rope; rotary_dim =
+ *                0 appends without rotation
+ *
+ * Rows outside every sequence (before cu_seqlens[0], from
+ * cu_seqlens[num_seqs] on) write nothing, in q_out as well, and no slot but
+ * the new tokens' is written.  Lengths and offsets out of range (a sequence
+ * shorter than its new tokens, longer than max_pages * page_size, offsets that
+ * decrease or pass `total`) and table entries outside the pool are flagged in
+ * the library status word (ta_device_status): a token with a bad length or
+ * offset writes nothing, one with a bad page writes its q_out row only.  Two
+ * tokens whose table entries name the same slot race.  Supported: d in {64,
+ * 128}, page_size in {8, 16, 32, 64}, rotary_dim a multiple of 16 in [0, d],
+ * Hq + 2 Hkv <= 65535, max_pages * page_size <= 2^30.  Allocates nothing.
+ */
+ta_status attn_paged_append(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
+                            const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *seq_lens,
+                            const int32_t *positions, const double *inv_freq, int page_size, int num_seqs,
+                            int total, int Hq, int Hkv, int d, int max_pages, int num_pages_total, int rotary_dim,
+                            int interleaved, float amplitude, int64_t q_stride_t, int64_t q_stride_h,
+                            int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                            ta_stream_t stream);
+
+/*
  * Bytes of device workspace attn_bwd needs (256-byte multiple): two fp32
  * values per query row, rows padded to a multiple of 128 per head.  Pure
  * host arithmetic; returns 0 for invalid sizes.

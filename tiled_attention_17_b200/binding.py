@@ -26,6 +26,7 @@ TA_DEV_BAD_SEQ_LEN = 4
 
 EXPORTS = ["ta_status_string", "ta_version", "ta_last_error", "attn_fwd", "attn_fwd_fp8", "attn_bwd_workspace_size",
            "attn_bwd",
+           "attn_rope", "attn_paged_append",
            "attn_paged_prefill", "attn_lse_merge", "attn_lse_merge_finish",
            "attn_paged_decode_workspace_size",
            "attn_paged_decode", "attn_paged_decode_noalloc", "attn_paged_decode_check", "attn_paged_gather_debug",
@@ -68,6 +69,10 @@ def load(path: str | None = None):
     L.attn_lse_merge.restype = i32
     L.attn_lse_merge_finish.argtypes = [vp, vp, i64, i32, vp]
     L.attn_lse_merge_finish.restype = i32
+    L.attn_rope.argtypes = [vp] * 4 + [i32] * 7 + [f32] + [i64] * 7 + [vp]
+    L.attn_rope.restype = i32
+    L.attn_paged_append.argtypes = [vp] * 11 + [i32] * 10 + [f32] + [i64] * 6 + [vp]
+    L.attn_paged_append.restype = i32
     L.attn_bwd_workspace_size.argtypes = [i32] * 3
     L.attn_bwd_workspace_size.restype = sz
     L.attn_bwd.argtypes = [vp] * 10 + [sz] + [i32] * 6 + [f32, i32, vp]
@@ -172,6 +177,31 @@ def attn_lse_merge_finish(acc_o, out, rows, d, stream=None, check=True) -> int:
     code = load().attn_lse_merge_finish(_ptr(acc_o), _ptr(out), int(rows), d, _stream(stream))
     if check:
         _check("attn_lse_merge_finish", code)
+    return code
+
+
+def attn_rope(x, y, positions, inv_freq, B, H, N, d, rotary_dim, interleaved, inverse, amplitude, x_stride_b,
+              x_stride_h, x_stride_n, y_stride_b, y_stride_h, y_stride_n, pos_stride_b, stream=None,
+              check=True) -> int:
+    code = load().attn_rope(_ptr(x), _ptr(y), _ptr(positions), _ptr(inv_freq), B, H, N, d, rotary_dim,
+                            int(interleaved), int(inverse), float(amplitude), x_stride_b, x_stride_h, x_stride_n,
+                            y_stride_b, y_stride_h, y_stride_n, pos_stride_b, _stream(stream))
+    if check:
+        _check("attn_rope", code)
+    return code
+
+
+def attn_paged_append(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, seq_lens, positions, inv_freq,
+                      page_size, num_seqs, total, Hq, Hkv, d, max_pages, num_pages_total, rotary_dim, interleaved,
+                      amplitude, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, stream=None,
+                      check=True) -> int:
+    code = load().attn_paged_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(block_table), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(positions),
+                                    _ptr(inv_freq), page_size, num_seqs, total, Hq, Hkv, d, max_pages,
+                                    num_pages_total, rotary_dim, int(interleaved), float(amplitude), q_stride_t,
+                                    q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, _stream(stream))
+    if check:
+        _check("attn_paged_append", code)
     return code
 
 
@@ -348,3 +378,137 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     attn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, ps, S, Hq, Hkv, d, max_pages, P, scale,
                       o, lse, workspace, workspace.numel(), stream)
     return o, lse, workspace
+
+
+def _scope(device, stream):
+    """The device and stream a convenience call allocates and launches on: the
+    tensors' device, and `stream` (a torch stream or its handle) or that
+    device's current one.  What the call allocates belongs to that stream."""
+    import contextlib
+
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _rows(name, t, shape=None):
+    """A bf16 CUDA tensor whose last dimension is contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a bf16 CUDA tensor with contiguous rows")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _ints(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _frequencies(inv_freq, device):
+    """rotary_dim of an inv_freq tensor (0 for None)."""
+    import torch
+    if inv_freq is None:
+        return 0
+    if inv_freq.dtype != torch.float64 or inv_freq.device != device or inv_freq.dim() != 1 \
+            or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous float64 tensor [rotary_dim / 2] on {device}")
+    return 2 * inv_freq.shape[0]
+
+
+def _rope(x, inv_freq, positions, interleaved, amplitude, out, stream, inverse):
+    import torch
+    if x.dim() != 4:
+        raise ValueError(f"x must be [B, H, N, d], got {tuple(x.shape)}")
+    B, H, N, d = x.shape
+    _rows("x", x)
+    rotary_dim = _frequencies(inv_freq, x.device)
+    pos_stride = 0
+    if positions is not None:
+        _ints("positions", positions, (N,) if positions.dim() == 1 else (B, N), x.device)
+        pos_stride = N if positions.dim() == 2 else 0
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=x.device)
+        elif _rows("out", out, x.shape).device != x.device:
+            raise ValueError("out must be on x's device")
+        xs, ys = x.stride(), out.stride()
+        attn_rope(x, out, positions, inv_freq, B, H, N, d, rotary_dim, interleaved, inverse, amplitude,
+                  xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], pos_stride)
+    return out
+
+
+def rope(x, inv_freq, positions=None, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """Rotary positions of x, a bf16 CUDA tensor or view [B, H, N, d] (e.g. the
+    heads of a fused projection's [B, N, heads, d] rows, transposed): the
+    rotated tensor, contiguous [B, H, N, d] as `attention` takes it, or written
+    to `out` (any view of that shape; x itself rotates in place).  inv_freq and
+    amplitude from `rope.frequencies` (None: copy only); positions int32 [N] or
+    [B, N], by default 0..N-1."""
+    return _rope(x, inv_freq, positions, interleaved, amplitude, out, stream, 0)
+
+
+def rope_backward(dout, inv_freq, positions=None, interleaved: bool = False, amplitude: float = 1.0, out=None,
+                  stream=None):
+    """The gradient of `rope`'s input for the output gradient dout (same
+    arguments); `out` may be a view of a fused projection's gradient rows."""
+    return _rope(dout, inv_freq, positions, interleaved, amplitude, out, stream, 1)
+
+
+def paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, q=None, q_out=None, inv_freq=None,
+                 positions=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """Write new tokens' keys (rotated) and values into the paged cache and
+    return their rotated queries (None without q).
+
+    k, v [total, Hkv, d] and q [total, Hq, d]: bf16 CUDA tensors or views with
+    contiguous rows; caches [P, Hkv, page, d]; block_table [S, max_pages];
+    seq_lens [S] the lengths after the append; cu_seqlens [S+1] packs the new
+    tokens as in `paged_prefill` (None: one token per sequence, total = S).
+    All index tensors int32.  inv_freq None appends without rotation."""
+    import torch
+    T, Hkv, d = k.shape
+    P, _, ps, _ = k_cache.shape
+    S, max_pages = block_table.shape
+    dev = k.device
+    _rows("k", k)
+    _rows("v", v, k.shape)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not _rows(name, t, (P, Hkv, ps, d)).is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _ints("block_table", block_table, (S, max_pages), dev)
+    _ints("seq_lens", seq_lens, (S,), dev)
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, (S + 1,), dev)
+    if positions is not None:
+        _ints("positions", positions, (T,), dev)
+    rotary_dim = _frequencies(inv_freq, dev)
+    Hq, qs = 0, (0, 0)
+    if q is not None:
+        Hq = q.shape[1]
+        _rows("q", q, (T, Hq, d))
+        qs = q.stride()
+    if any(t is not None and t.device != dev for t in (v, k_cache, v_cache, q, q_out)):
+        raise ValueError("all tensors must be on one device")
+    with _scope(dev, stream):
+        if q is None:
+            q_out = None
+        elif q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        elif not _rows("q_out", q_out, (T, Hq, d)).is_contiguous():
+            raise ValueError("q_out must be contiguous")
+        ks, vs = k.stride(), v.stride()
+        attn_paged_append(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, seq_lens, positions, inv_freq,
+                          ps, S, T, Hq, Hkv, d, max_pages, P, rotary_dim, interleaved, amplitude, qs[0], qs[1],
+                          ks[0], ks[1], vs[0], vs[1])
+    return q_out

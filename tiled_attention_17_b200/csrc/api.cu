@@ -284,6 +284,71 @@ ta_status attn_lse_merge_finish(const float* acc_o, void* out, int64_t rows, int
   return launch_lse_merge_finish(acc_o, out, rows, d, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Checks shared by the two calls that rotate.
+static ta_status validate_rotation(const double* inv_freq, int d, int rotary_dim, int interleaved, float amplitude) {
+  if (d <= 0 || rotary_dim < 0 || rotary_dim > d || (interleaved != 0 && interleaved != 1)) return TA_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude)) return TA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return TA_ERR_UNSUPPORTED;
+  if (rotary_dim % 16 != 0) return TA_ERR_UNSUPPORTED;   // 16-byte vectors hold whole pairs or whole halves
+  if (rotary_dim > 0 && (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))) return TA_ERR_INVALID_ARG;
+  return TA_OK;
+}
+
+ta_status attn_rope(const void* x, void* y, const int32_t* positions, const double* inv_freq, int B, int H, int N,
+                    int d, int rotary_dim, int interleaved, int inverse, float amplitude, int64_t x_stride_b,
+                    int64_t x_stride_h, int64_t x_stride_n, int64_t y_stride_b, int64_t y_stride_h,
+                    int64_t y_stride_n, int64_t pos_stride_b, ta_stream_t stream) {
+  if (B < 0 || H < 0 || N < 0 || (inverse != 0 && inverse != 1)) return TA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N > INT32_MAX || H > 65535) return TA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * N == 0 || H == 0) return TA_OK;
+  const ta_status st = validate_rotation(inv_freq, d, rotary_dim, interleaved, amplitude);
+  if (st != TA_OK) return st;
+  if (!x || !y || !aligned16(x) || !aligned16(y) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return TA_ERR_INVALID_ARG;
+  const int64_t xs[3] = {x_stride_b, x_stride_h, x_stride_n}, ys[3] = {y_stride_b, y_stride_h, y_stride_n};
+  const int size[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i) {
+    if (xs[i] % 8 != 0 || ys[i] % 8 != 0) return TA_ERR_INVALID_ARG;
+    if (size[i] > 1 && ys[i] == 0) return TA_ERR_INVALID_ARG;                   // rows written twice
+    if (size[i] > 1 && x == y && xs[i] != ys[i]) return TA_ERR_INVALID_ARG;   // in place: the same rows
+  }
+  return launch_rope(x, y, positions, inv_freq, B, H, N, d, rotary_dim, interleaved, inverse, amplitude, xs, ys,
+                     pos_stride_b, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ta_status attn_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                            const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                            const int32_t* positions, const double* inv_freq, int page_size, int num_seqs, int total,
+                            int Hq, int Hkv, int d, int max_pages, int num_pages_total, int rotary_dim,
+                            int interleaved, float amplitude, int64_t q_stride_t, int64_t q_stride_h,
+                            int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                            ta_stream_t stream) {
+  if (num_seqs < 0 || total < 0 || Hkv <= 0 || page_size <= 0 || max_pages <= 0 || num_pages_total <= 0)
+    return TA_ERR_INVALID_ARG;
+  if (q ? Hq <= 0 : Hq < 0) return TA_ERR_INVALID_ARG;
+  if (!cu_seqlens && total != num_seqs) return TA_ERR_INVALID_ARG;
+  const ta_status st = validate_rotation(inv_freq, d, rotary_dim, interleaved, amplitude);
+  if (st != TA_OK) return st;
+  if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64) return TA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_size > (1 << 30) || static_cast<long long>(Hq) + 2ll * Hkv > 65535)
+    return TA_ERR_UNSUPPORTED;
+  if (total == 0 || num_seqs == 0) return TA_OK;
+  if (!k || !v || !k_cache || !v_cache || !block_table || !seq_lens || (q && !q_out)) return TA_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_cache),
+                        static_cast<const void*>(v_cache)})
+    if (!aligned16(p)) return TA_ERR_INVALID_ARG;
+  for (const int32_t* p : {block_table, cu_seqlens, seq_lens, positions})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return TA_ERR_INVALID_ARG;
+  const int64_t strides[6] = {q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h};
+  for (int i = q ? 0 : 2; i < 6; ++i)
+    if (strides[i] % 8 != 0) return TA_ERR_INVALID_ARG;
+  if (q && q == q_out && ((total > 1 && q_stride_t != static_cast<int64_t>(Hq) * d) || (Hq > 1 && q_stride_h != d)))
+    return TA_ERR_INVALID_ARG;
+  return launch_paged_append(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, seq_lens, positions, inv_freq,
+                             page_size, num_seqs, total, Hq, Hkv, d, max_pages, num_pages_total, rotary_dim,
+                             interleaved, amplitude, strides, reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t attn_bwd_workspace_size(int B, int Hq, int Nq) {
   if (B < 0 || Hq <= 0 || Nq < 0) return 0;
   if (static_cast<long long>(B) * Hq > INT32_MAX / 2 || Nq > (1 << 30)) return 0;

@@ -117,6 +117,18 @@ ta_status launch_lse_merge(float* acc_o, float* acc_lse, const void* part_o, con
                            int d, int first, cudaStream_t stream);
 ta_status launch_lse_merge_finish(const float* acc_o, void* out, int64_t rows, int d, cudaStream_t stream);
 
+// strides in elements: {batch, head, token}
+ta_status launch_rope(const void* x, void* y, const int32_t* positions, const double* inv_freq, int B, int H, int N,
+                      int d, int rotary_dim, int interleaved, int inverse, float amplitude, const int64_t* x_strides,
+                      const int64_t* y_strides, int64_t pos_stride, cudaStream_t stream);
+
+// strides in elements: {q token, q head, k token, k head, v token, v head}
+ta_status launch_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                              const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                              const int32_t* positions, const double* inv_freq, int page_size, int num_seqs,
+                              int total, int Hq, int Hkv, int d, int max_pages, int num_pages_total, int rotary_dim,
+                              int interleaved, float amplitude, const int64_t* strides, cudaStream_t stream);
+
 size_t bwd_workspace_bytes(int B, int Hq, int Nq);
 ta_status launch_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
                           const float* lse, void* dq, void* dk, void* dv, void* workspace, int B, int Hq, int Hkv,
