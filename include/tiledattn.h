@@ -374,6 +374,53 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
                                     ta_stream_t stream);
 
 /*
+ * attn_paged_decode_shared - attn_paged_decode for a batch in which groups of
+ * sequences share a long prefix: the prefix of a group is read and multiplied
+ * once for all of its sequences (on the tensor cores), the rest of each
+ * sequence as in attn_paged_decode, and the two are joined by their
+ * log-sum-exp (exact: FlashAttention optimisation article, section 3.2.2).
+ *
+ *   q, o, lse, k_cache, v_cache, block_table, seq_lens: as attn_paged_decode
+ *                (block-table rows and lengths cover the whole sequence, the
+ *                prefix included)
+ *   group_offsets [num_groups + 1] int32, nondecreasing within [0, num_seqs]:
+ *                group g is sequences [group_offsets[g], group_offsets[g+1]),
+ *                possibly none (its length is then ignored).  Sequences
+ *                outside every group are ordinary
+ *   prefix_lens  [num_groups] int32: the first prefix_lens[g] tokens of the
+ *                group's sequences are the same.  They are read through the
+ *                block-table row of the group's FIRST sequence (whatever its
+ *                own length), every later token through the sequence's own
+ *                row.  Any length, inside a page too; 0 shares nothing.  A
+ *                sequence shorter than the prefix takes all its tokens from its
+ *                own row
+ *   max_own_len  most tokens any sequence reads through its own row (those
+ *                after the prefix; all of them where there is none); sizes the
+ *                grid and the workspace.  A sequence with more is cut there
+ *                and flagged
+ *   workspace    >= attn_paged_decode_shared_workspace_size(...) bytes,
+ *                256-byte aligned, as in attn_paged_decode; the status word is
+ *                read by attn_paged_decode_check.  Must not be shared by calls
+ *                that may run concurrently
+ *
+ * Supported: the shapes of attn_paged_decode, max_pages * page_size <= 2^30,
+ * num_groups <= 65535, num_pages_total * Hkv < 2^31.  Pool rows behind a
+ * prefix, or behind a sequence, are not used and may hold anything; the prefix
+ * rows themselves are used by every sequence of the group.  Out-of-range
+ * lengths, prefix lengths and table entries are clamped on the device and
+ * flagged; offsets that decrease or leave the batch are flagged and no prefix
+ * is shared.  The result does not depend on scheduling.
+ */
+size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d, int max_own_len,
+                                               int page_size);
+ta_status attn_paged_decode_shared(const void *q, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *group_offsets, const int32_t *prefix_lens, int page_size,
+                                   int num_seqs, int num_groups, int max_own_len, int Hq, int Hkv, int d,
+                                   int max_pages, int num_pages_total, float scale, void *o, float *lse,
+                                   void *workspace, size_t workspace_bytes, ta_stream_t stream);
+
+/*
  * Checked mode for paged decode: waits for `stream`, reads the status word the
  * last attn_paged_decode wrote into `workspace`, stores it in *flags (host
  * pointer, may be NULL) and returns TA_ERR_BAD_BLOCK_TABLE or

@@ -29,6 +29,7 @@ EXPORTS = ["ta_status_string", "ta_version", "ta_last_error", "attn_fwd", "attn_
            "attn_rope", "attn_paged_append",
            "attn_paged_prefill", "attn_lse_merge", "attn_lse_merge_finish",
            "attn_paged_decode_workspace_size",
+           "attn_paged_decode_shared_workspace_size", "attn_paged_decode_shared",
            "attn_paged_decode", "attn_paged_decode_noalloc", "attn_paged_decode_check", "attn_paged_gather_debug",
            "ta_device_status", "ta_selftest_bounded_wait", "ta_exp2_poly_debug"]
 
@@ -81,6 +82,10 @@ def load(path: str | None = None):
     L.attn_paged_decode_workspace_size.restype = sz
     L.attn_paged_decode.argtypes = [vp, vp, vp, vp, vp] + [i32] * 7 + [f32, vp, vp, vp, sz, vp]
     L.attn_paged_decode.restype = i32
+    L.attn_paged_decode_shared_workspace_size.argtypes = [i32] * 7
+    L.attn_paged_decode_shared_workspace_size.restype = sz
+    L.attn_paged_decode_shared.argtypes = [vp] * 7 + [i32] * 9 + [f32, vp, vp, vp, sz, vp]
+    L.attn_paged_decode_shared.restype = i32
     L.attn_paged_decode_noalloc.argtypes = [vp, vp, vp, vp, vp] + [i32] * 7 + [f32, vp, vp, vp]
     L.attn_paged_decode_noalloc.restype = i32
     L.attn_paged_decode_check.argtypes = [vp, ctypes.POINTER(u32), vp]
@@ -244,6 +249,22 @@ def attn_paged_decode_noalloc(q, k_cache, v_cache, block_table, seq_lens, page_s
                                             num_pages_total, float(scale), _ptr(o), _ptr(lse), _stream(stream))
     if check:
         _check("attn_paged_decode_noalloc", code)
+    return code
+
+
+def attn_paged_decode_shared_workspace_size(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size) -> int:
+    return load().attn_paged_decode_shared_workspace_size(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size)
+
+
+def attn_paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, page_size,
+                             num_seqs, num_groups, max_own_len, Hq, Hkv, d, max_pages, num_pages_total, scale, o, lse,
+                             workspace, workspace_bytes, stream=None, check=True) -> int:
+    code = load().attn_paged_decode_shared(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                           _ptr(group_offsets), _ptr(prefix_lens), page_size, num_seqs, num_groups,
+                                           max_own_len, Hq, Hkv, d, max_pages, num_pages_total, float(scale), _ptr(o),
+                                           _ptr(lse), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check("attn_paged_decode_shared", code)
     return code
 
 
@@ -512,3 +533,45 @@ def paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None,
                           ps, S, T, Hq, Hkv, d, max_pages, P, rotary_dim, interleaved, amplitude, qs[0], qs[1],
                           ks[0], ks[1], vs[0], vs[1])
     return q_out
+
+
+def paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens,
+                        max_own_len: int | None = None, scale: float | None = None, workspace=None, out=None,
+                        lse=None, stream=None):
+    """`paged_decode` where groups of sequences share a prefix, which is read
+    once per group: group g is sequences [group_offsets[g],
+    group_offsets[g+1]), whose first prefix_lens[g] tokens are the same (read
+    through the first sequence's block-table row).  max_own_len: most tokens a
+    sequence has after its prefix (by default what the table can hold).
+    group_offsets [G+1] and prefix_lens [G] are int32 device tensors, the rest
+    as `paged_decode`; returns (o, lse, workspace)."""
+    import torch
+    S, Hq, d = q.shape
+    P, Hkv, ps, _ = k_cache.shape
+    max_pages = block_table.shape[1]
+    groups = prefix_lens.shape[0]
+    dev = q.device
+    for name, t, shape in (("q", q, (S, Hq, d)), ("k_cache", k_cache, (P, Hkv, ps, d)),
+                           ("v_cache", v_cache, (P, Hkv, ps, d))):
+        if not _rows(name, t, shape).is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be contiguous and on {dev}")
+    _ints("block_table", block_table, (S, max_pages), dev)
+    _ints("seq_lens", seq_lens, (S,), dev)
+    _ints("group_offsets", group_offsets, (groups + 1,), dev)
+    _ints("prefix_lens", prefix_lens, (groups,), dev)
+    if max_own_len is None:
+        max_own_len = max_pages * ps
+    if scale is None:
+        scale = d ** -0.5
+    with _scope(dev, stream):
+        if workspace is None:
+            need = attn_paged_decode_shared_workspace_size(S, groups, Hq, Hkv, d, max_own_len, ps)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
+        attn_paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, ps, S, groups,
+                                 max_own_len, Hq, Hkv, d, max_pages, P, scale, out, lse, workspace,
+                                 workspace.numel() * workspace.element_size())
+    return out, lse, workspace

@@ -141,6 +141,32 @@ ta_status encode_rows_chunked(CUtensorMap* map, const void* base, int d, int row
   return encode_bf16_tiled(map, base, 4, dims, strides, box);
 }
 
+ta_status encode_pool_maps(CUtensorMap* k_map, CUtensorMap* v_map, const void* k_cache, const void* v_cache, int d,
+                           int page_size, int Hkv, int num_pages) {
+  const uint64_t row = static_cast<uint64_t>(d) * 2, ps = static_cast<uint64_t>(page_size);
+  ta_status st;
+  if (d == 64) {
+    const uint64_t dims[4] = {64, ps, static_cast<uint64_t>(Hkv), static_cast<uint64_t>(num_pages)};
+    const uint64_t strides[3] = {row, ps * row, Hkv * ps * row};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(page_size), 1, 1};
+    if ((st = encode_bf16_tiled(k_map, k_cache, 4, dims, strides, box)) != TA_OK) return st;
+    return encode_bf16_tiled(v_map, v_cache, 4, dims, strides, box);
+  }
+  // K: [P, Hkv, page, 128] seen as 5-D {16 columns, 8 rows, 8 column groups, page / 8 row
+  // groups, P * Hkv (page, head) blocks}, box {16, 8, 8, page / 8, 1}, 32-byte swizzle: one
+  // copy lands a page as [row group][column group][8 rows][32 B]
+  const uint64_t dk[5] = {16, 8, 8, ps / 8, static_cast<uint64_t>(num_pages) * Hkv};
+  const uint64_t sk[4] = {row, 32, 8 * row, ps * row};
+  const uint32_t bk[5] = {16, 8, 8, static_cast<uint32_t>(page_size / 8), 1};
+  if ((st = encode_bf16_tiled_sw32(k_map, k_cache, 5, dk, sk, bk)) != TA_OK) return st;
+  // V: [P, Hkv, page, (2 chunks of 64)] seen as 5-D {64, page, chunk, Hkv, P}, so that one box
+  // {64, page, 2, 1, 1} lands a page as [chunk][page rows][128 B]
+  const uint64_t dv[5] = {64, ps, 2, static_cast<uint64_t>(Hkv), static_cast<uint64_t>(num_pages)};
+  const uint64_t sv[4] = {row, 128, ps * row, Hkv * ps * row};
+  const uint32_t bv[5] = {64, static_cast<uint32_t>(page_size), 2, 1, 1};
+  return encode_bf16_tiled(v_map, v_cache, 5, dv, sv, bv);
+}
+
 static thread_local char g_last_error[256] = "";
 
 ta_status fail(ta_status code, const char* where, cudaError_t err) {
@@ -432,6 +458,56 @@ ta_status attn_paged_decode(const void* q, const void* k_cache, const void* v_ca
   if (workspace_bytes < plan.bytes) return TA_ERR_INVALID_ARG;
   return launch_paged_decode(q, k_cache, v_cache, block_table, seq_lens, page_size, num_seqs, Hq, Hkv, d, max_pages,
                              num_pages_total, scale, o, lse, workspace, plan, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static ta_status validate_shared_shape(int page_size, int num_seqs, int num_groups, int max_own_len, int Hq, int Hkv,
+                                       int d, int max_pages, int num_pages_total) {
+  const ta_status st = validate_decode_shape(page_size, num_seqs, Hq, Hkv, d, max_pages, num_pages_total);
+  if (st != TA_OK) return st;
+  if (num_groups < 0 || max_own_len < 0) return TA_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * page_size > (1 << 30) || num_groups > 65535) return TA_ERR_UNSUPPORTED;
+  if (max_own_len > max_pages * page_size) return TA_ERR_INVALID_ARG;
+  // the K copies address a (page, KV head) block by one 32-bit coordinate
+  if (static_cast<long long>(num_pages_total) * Hkv > INT32_MAX) return TA_ERR_UNSUPPORTED;
+  return TA_OK;
+}
+
+size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d, int max_own_len,
+                                               int page_size) {
+  SharedPlan plan;
+  if (!make_shared_plan(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size, &plan)) return 0;
+  return plan.bytes;
+}
+
+ta_status attn_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* group_offsets,
+                                   const int32_t* prefix_lens, int page_size, int num_seqs, int num_groups,
+                                   int max_own_len, int Hq, int Hkv, int d, int max_pages, int num_pages_total,
+                                   float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                   ta_stream_t stream) {
+  const ta_status st = validate_shared_shape(page_size, num_seqs, num_groups, max_own_len, Hq, Hkv, d, max_pages,
+                                             num_pages_total);
+  if (st != TA_OK) return st;
+  if (!std::isfinite(scale) || scale < 0.f) return TA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return TA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !workspace ||
+      (num_groups > 0 && (!group_offsets || !prefix_lens)))
+    return TA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+      (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return TA_ERR_INVALID_ARG;
+  for (const int32_t* p : {block_table, seq_lens, group_offsets, prefix_lens})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return TA_ERR_INVALID_ARG;
+  SharedPlan plan;
+  if (!make_shared_plan(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size, &plan)) return TA_ERR_UNSUPPORTED;
+  if (workspace_bytes < plan.bytes) {
+    char msg[160];
+    snprintf(msg, sizeof msg, "attn_paged_decode_shared: workspace needs %zu bytes, 256-byte aligned", plan.bytes);
+    return fail(TA_ERR_INVALID_ARG, msg);
+  }
+  return launch_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, page_size,
+                              num_seqs, num_groups, max_own_len, Hq, Hkv, d, max_pages, num_pages_total, scale, o,
+                              lse, workspace, plan, reinterpret_cast<cudaStream_t>(stream));
 }
 
 ta_status attn_paged_decode_check(const void* workspace, unsigned* flags, ta_stream_t stream) {
