@@ -376,9 +376,10 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
 /*
  * attn_paged_decode_shared - attn_paged_decode for a batch in which groups of
  * sequences share a long prefix: the prefix of a group is read and multiplied
- * once for all of its sequences (on the tensor cores), the rest of each
- * sequence as in attn_paged_decode, and the two are joined by their
- * log-sum-exp (exact: FlashAttention optimisation article, section 3.2.2).
+ * once for all of its sequences, and joined with the rest of each sequence by
+ * their log-sum-exp (exact: FlashAttention optimisation article, section
+ * 3.2.2).  Both run on the tensor cores with the softmax weights rounded to
+ * bf16 (as attn_fwd), sums in fp32.
  *
  *   q, o, lse, k_cache, v_cache, block_table, seq_lens: as attn_paged_decode
  *                (block-table rows and lengths cover the whole sequence, the
@@ -395,9 +396,9 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
  *                sequence shorter than the prefix takes all its tokens from its
  *                own row
  *   max_own_len  most tokens any sequence reads through its own row (those
- *                after the prefix; all of them where there is none); sizes the
- *                grid and the workspace.  A sequence with more is cut there
- *                and flagged
+ *                after the prefix; all of them where there is none), at most
+ *                max_pages * page_size.  A sequence with more is cut there and
+ *                flagged: a wrong length or prefix costs no more than that
  *   workspace    >= attn_paged_decode_shared_workspace_size(...) bytes,
  *                256-byte aligned, as in attn_paged_decode; the status word is
  *                read by attn_paged_decode_check.  Must not be shared by calls
@@ -411,8 +412,7 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
  * flagged; offsets that decrease or leave the batch are flagged and no prefix
  * is shared.  The result does not depend on scheduling.
  */
-size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d, int max_own_len,
-                                               int page_size);
+size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d);
 ta_status attn_paged_decode_shared(const void *q, const void *k_cache, const void *v_cache,
                                    const int32_t *block_table, const int32_t *seq_lens,
                                    const int32_t *group_offsets, const int32_t *prefix_lens, int page_size,

@@ -109,8 +109,7 @@ class Batch:
                 dev(get("offsets", self.offsets)), dev(get("prefix", self.prefix))]
         max_own = get("max_own", self.max_own)
         if workspace is None:
-            need = binding.attn_paged_decode_shared_workspace_size(self.S, len(self.prefix), self.Hq, self.Hkv, self.d,
-                                                                   max_own, self.ps)
+            need = binding.attn_paged_decode_shared_workspace_size(self.S, len(self.prefix), self.Hq, self.Hkv, self.d)
             workspace = torch.full((need,), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is not written
         torch.cuda.synchronize()
         o, lse, ws = binding.paged_decode_shared(*args, max_own_len=max_own, scale=scale, workspace=workspace,

@@ -12,7 +12,7 @@ def lib():
 
 def test_shared_validation(lib):
     a = 256
-    ws = lib.attn_paged_decode_shared_workspace_size(4, 2, 8, 2, 128, 100, 16)
+    ws = lib.attn_paged_decode_shared_workspace_size(4, 2, 8, 2, 128)
 
     def call(**kw):
         g = dict(q=a, kc=a, vc=a, bt=a, sl=a, go=a, pl=a, ps=16, S=4, NG=2, own=100, Hq=8, Hkv=2, d=128, mp=64, P=100,
@@ -44,14 +44,14 @@ def test_shared_validation(lib):
 
 def test_shared_workspace_size(lib):
     size = lib.attn_paged_decode_shared_workspace_size
-    one = size(64, 1, 32, 8, 128, 512, 16)
+    one = size(64, 1, 32, 8, 128)
     assert one % 256 == 0
-    # one 256-row block per KV head and (148 SMs) one partial more per CTA, 128 KB each, and the own-key partials
-    assert one >= (8 + 148) * 256 * 128 * 4
-    assert size(64, 0, 32, 8, 128, 512, 16) < one           # no groups: no prefix partials
-    assert size(64, 1, 32, 8, 128, 0, 16) < one             # no own keys
-    assert size(64, 1, 30, 8, 128, 512, 16) == 0
-    assert size(64, 1, 32, 8, 96, 512, 16) == 0
-    assert size(64, 1, 32, 8, 128, 512, 12) == 0
-    assert size(65536, 1, 32, 8, 128, 512, 16) == 0
-    assert size(64, 1, 32, 8, 128, -1, 16) == 0
+    # one 256-row block per KV head and (148 SMs) one more per CTA, 128 KB each; two partials of
+    # 4 rows for every sequence and KV head
+    assert one >= (8 + 148) * 256 * 128 * 4 + 64 * 8 * 2 * 4 * 128 * 4
+    assert size(64, 0, 32, 8, 128) < one - 148 * 256 * 128 * 4    # no groups: no prefix partials
+    assert size(64, 1, 30, 8, 128) == 0
+    assert size(64, 1, 32, 8, 96) == 0
+    assert size(65536, 1, 32, 8, 128) == 0
+    assert size(64, 65536, 32, 8, 128) == 0
+    assert size(64, -1, 32, 8, 128) == 0

@@ -82,7 +82,7 @@ def load(path: str | None = None):
     L.attn_paged_decode_workspace_size.restype = sz
     L.attn_paged_decode.argtypes = [vp, vp, vp, vp, vp] + [i32] * 7 + [f32, vp, vp, vp, sz, vp]
     L.attn_paged_decode.restype = i32
-    L.attn_paged_decode_shared_workspace_size.argtypes = [i32] * 7
+    L.attn_paged_decode_shared_workspace_size.argtypes = [i32] * 5
     L.attn_paged_decode_shared_workspace_size.restype = sz
     L.attn_paged_decode_shared.argtypes = [vp] * 7 + [i32] * 9 + [f32, vp, vp, vp, sz, vp]
     L.attn_paged_decode_shared.restype = i32
@@ -252,8 +252,8 @@ def attn_paged_decode_noalloc(q, k_cache, v_cache, block_table, seq_lens, page_s
     return code
 
 
-def attn_paged_decode_shared_workspace_size(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size) -> int:
-    return load().attn_paged_decode_shared_workspace_size(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size)
+def attn_paged_decode_shared_workspace_size(num_seqs, num_groups, Hq, Hkv, d) -> int:
+    return load().attn_paged_decode_shared_workspace_size(num_seqs, num_groups, Hq, Hkv, d)
 
 
 def attn_paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, page_size,
@@ -565,7 +565,7 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
         scale = d ** -0.5
     with _scope(dev, stream):
         if workspace is None:
-            need = attn_paged_decode_shared_workspace_size(S, groups, Hq, Hkv, d, max_own_len, ps)
+            need = attn_paged_decode_shared_workspace_size(S, groups, Hq, Hkv, d)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         if out is None:
             out = torch.empty_like(q)

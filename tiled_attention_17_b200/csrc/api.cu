@@ -141,32 +141,6 @@ ta_status encode_rows_chunked(CUtensorMap* map, const void* base, int d, int row
   return encode_bf16_tiled(map, base, 4, dims, strides, box);
 }
 
-ta_status encode_pool_maps(CUtensorMap* k_map, CUtensorMap* v_map, const void* k_cache, const void* v_cache, int d,
-                           int page_size, int Hkv, int num_pages) {
-  const uint64_t row = static_cast<uint64_t>(d) * 2, ps = static_cast<uint64_t>(page_size);
-  ta_status st;
-  if (d == 64) {
-    const uint64_t dims[4] = {64, ps, static_cast<uint64_t>(Hkv), static_cast<uint64_t>(num_pages)};
-    const uint64_t strides[3] = {row, ps * row, Hkv * ps * row};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(page_size), 1, 1};
-    if ((st = encode_bf16_tiled(k_map, k_cache, 4, dims, strides, box)) != TA_OK) return st;
-    return encode_bf16_tiled(v_map, v_cache, 4, dims, strides, box);
-  }
-  // K: [P, Hkv, page, 128] seen as 5-D {16 columns, 8 rows, 8 column groups, page / 8 row
-  // groups, P * Hkv (page, head) blocks}, box {16, 8, 8, page / 8, 1}, 32-byte swizzle: one
-  // copy lands a page as [row group][column group][8 rows][32 B]
-  const uint64_t dk[5] = {16, 8, 8, ps / 8, static_cast<uint64_t>(num_pages) * Hkv};
-  const uint64_t sk[4] = {row, 32, 8 * row, ps * row};
-  const uint32_t bk[5] = {16, 8, 8, static_cast<uint32_t>(page_size / 8), 1};
-  if ((st = encode_bf16_tiled_sw32(k_map, k_cache, 5, dk, sk, bk)) != TA_OK) return st;
-  // V: [P, Hkv, page, (2 chunks of 64)] seen as 5-D {64, page, chunk, Hkv, P}, so that one box
-  // {64, page, 2, 1, 1} lands a page as [chunk][page rows][128 B]
-  const uint64_t dv[5] = {64, ps, 2, static_cast<uint64_t>(Hkv), static_cast<uint64_t>(num_pages)};
-  const uint64_t sv[4] = {row, 128, ps * row, Hkv * ps * row};
-  const uint32_t bv[5] = {64, static_cast<uint32_t>(page_size), 2, 1, 1};
-  return encode_bf16_tiled(v_map, v_cache, 5, dv, sv, bv);
-}
-
 static thread_local char g_last_error[256] = "";
 
 ta_status fail(ta_status code, const char* where, cudaError_t err) {
@@ -472,10 +446,9 @@ static ta_status validate_shared_shape(int page_size, int num_seqs, int num_grou
   return TA_OK;
 }
 
-size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d, int max_own_len,
-                                               int page_size) {
+size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d) {
   SharedPlan plan;
-  if (!make_shared_plan(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size, &plan)) return 0;
+  if (!make_shared_plan(num_seqs, num_groups, Hq, Hkv, d, &plan)) return 0;
   return plan.bytes;
 }
 
@@ -499,7 +472,7 @@ ta_status attn_paged_decode_shared(const void* q, const void* k_cache, const voi
   for (const int32_t* p : {block_table, seq_lens, group_offsets, prefix_lens})
     if (reinterpret_cast<uintptr_t>(p) & 3u) return TA_ERR_INVALID_ARG;
   SharedPlan plan;
-  if (!make_shared_plan(num_seqs, num_groups, Hq, Hkv, d, max_own_len, page_size, &plan)) return TA_ERR_UNSUPPORTED;
+  if (!make_shared_plan(num_seqs, num_groups, Hq, Hkv, d, &plan)) return TA_ERR_UNSUPPORTED;
   if (workspace_bytes < plan.bytes) {
     char msg[160];
     snprintf(msg, sizeof msg, "attn_paged_decode_shared: workspace needs %zu bytes, 256-byte aligned", plan.bytes);

@@ -83,59 +83,11 @@ struct DecodeArgs {
   float* part_o;
   float* part_lse;
   unsigned* status;
-  // own-keys form (kOwn): sequence s attends only to its keys from
-  // own_start[s] on (the earlier ones are a prefix handled elsewhere), at most
-  // max_own of them; splits count from the page that holds own_start[s]
-  const int32_t* own_start;
-  int max_own;
 };
 
 __device__ __forceinline__ int clamp_len(int len, const DecodeArgs& a) {
   const int cap = a.max_pages * a.page_size;
   return len < 0 ? 0 : (len > cap ? cap : len);
-}
-
-// The keys one split CTA reads: [t_begin, t_end) of its sequence, from page
-// first_page on; the first `skip` of them (a prefix that ends inside a page)
-// get no weight.
-struct SplitRange {
-  int t_begin, t_end, first_page, skip;
-  bool empty;
-};
-template <bool kOwn>
-__device__ __forceinline__ SplitRange split_range(const DecodeArgs& a, int split, int hkv, int seq) {
-  const int raw_len = __ldg(a.seq_lens + seq);
-  int len = clamp_len(raw_len, a);
-  bool bad = raw_len != len;
-  int start = 0;
-  if constexpr (kOwn) {
-    start = __ldg(a.own_start + seq);
-    if (len - start > a.max_own) {
-      bad = true;
-      len = start + a.max_own;
-    }
-  }
-  if (bad && split == 0 && hkv == 0 && threadIdx.x == 0) atomicOr(a.status, kDevBadSeqLen);
-  const int page0 = start / a.page_size, base = page0 * a.page_size;
-  const int split_tokens = a.split_pages * a.page_size;
-  SplitRange r;
-  r.t_begin = base + split * split_tokens;
-  r.empty = r.t_begin >= len || start >= len;
-  r.t_end = min(len, r.t_begin + split_tokens);
-  r.first_page = page0 + split * a.split_pages;
-  r.skip = split == 0 ? start - base : 0;
-  return r;
-}
-
-// The own-keys kernels run as programmatic dependents of the prefix kernel and
-// do not wait for it; the combine, their own dependent, needs both.  One CTA
-// waits for the prefix kernel before it leaves, so the grid cannot complete
-// earlier (the others give their SM to the next split at once).
-template <bool kOwn>
-__device__ __forceinline__ void leave_split(int split, int hkv, int seq) {
-  if constexpr (kOwn) {
-    if (split == 0 && hkv == 0 && seq == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -229,7 +181,7 @@ __device__ __forceinline__ void segment_allreduce(float (&v)[G], uint32_t mask, 
 
 constexpr float kDecRescaleLog2 = 8.0f;   // keep a stale max until it is exceeded by 2^8
 
-template <int D, int G, bool kOwn>
+template <int D, int G>
 __global__ void __launch_bounds__(kSplitThreads, (G <= 4 ? 2 : 1)) decode_split_kernel(const DecodeArgs a) {
   using L = DecodeLayout<D>;
   constexpr int LPR = L::kLanesPerRow;
@@ -239,14 +191,15 @@ __global__ void __launch_bounds__(kSplitThreads, (G <= 4 ? 2 : 1)) decode_split_
   extern __shared__ __align__(1024) uint8_t smem[];
 
   const int split = blockIdx.x, hkv = blockIdx.y, seq = blockIdx.z;
-  const SplitRange range = split_range<kOwn>(a, split, hkv, seq);
-  if (range.empty) {   // CTA-uniform: nothing in this split
-    leave_split<kOwn>(split, hkv, seq);
-    return;
-  }
-  const int t_begin = range.t_begin, t_end = range.t_end, skip = kOwn ? range.skip : 0;
+  const int raw_len = __ldg(a.seq_lens + seq);
+  const int len = clamp_len(raw_len, a);
+  if (raw_len != len && split == 0 && hkv == 0 && threadIdx.x == 0) atomicOr(a.status, kDevBadSeqLen);
+  const int split_tokens = a.split_pages * a.page_size;
+  const int t_begin = split * split_tokens;
+  if (t_begin >= len) return;  // CTA-uniform: nothing in this split
+  const int t_end = min(len, t_begin + split_tokens);
   const int n_chunks = (t_end - t_begin + kChunkTokens - 1) / kChunkTokens;
-  const int split_first_page = range.first_page;
+  const int split_first_page = split * a.split_pages;
   const int split_npages = (t_end - t_begin + a.page_size - 1) / a.page_size;
   const int pages_per_chunk = kChunkTokens / a.page_size;
 
@@ -326,7 +279,7 @@ __global__ void __launch_bounds__(kSplitThreads, (G <= 4 ? 2 : 1)) decode_split_
         const int row0 = warp * kRowsPerWarp + p * SEGS;
         if (row0 >= valid) break;                          // warp-uniform
         const int row = row0 + seg;
-        const bool rv = row < valid && (!kOwn || c > 0 || row >= skip);
+        const bool rv = row < valid;
         // ---- q . k for the G heads (16-byte slice per lane), summed over the row's lanes
         const uint4 ku = *reinterpret_cast<const uint4*>(sK + row * L::kRowBytes + lane_r * 16);
         const float2 k0 = bf16x2_to_f2(ku.x), k1 = bf16x2_to_f2(ku.y);
@@ -398,10 +351,7 @@ __global__ void __launch_bounds__(kSplitThreads, (G <= 4 ? 2 : 1)) decode_split_
     }
   }
   __syncthreads();
-  if (*abort_flag) {
-    leave_split<kOwn>(split, hkv, seq);
-    return;
-  }
+  if (*abort_flag) return;
   const float c2 = a.scale_log2;
   const size_t row0 = (static_cast<size_t>(seq) * a.Hq + hkv * G) * a.max_splits + split;
   for (int idx = tid; idx < G * D; idx += kSplitThreads) {
@@ -418,7 +368,6 @@ __global__ void __launch_bounds__(kSplitThreads, (G <= 4 ? 2 : 1)) decode_split_
     a.part_o[(row0 + static_cast<size_t>(g) * a.max_splits) * D + col] = o / tot;
     if (col == 0) a.part_lse[row0 + static_cast<size_t>(g) * a.max_splits] = fmaf(M, a.scale, __logf(tot));
   }
-  leave_split<kOwn>(split, hkv, seq);
 }
 
 // ---------------------------------------------------------------------------
@@ -462,21 +411,21 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel_shared(uint32_t addr, uint3
   return old;
 }
 
-template <bool kOwn>
 __global__ void __launch_bounds__(kG4Threads, 2) decode_split_g4_kernel(const DecodeArgs a) {
   using L = G4Layout;
   constexpr int D = 128;
   extern __shared__ __align__(1024) uint8_t smem[];
 
   const int split = blockIdx.x, hkv = blockIdx.y, seq = blockIdx.z;
-  const SplitRange range = split_range<kOwn>(a, split, hkv, seq);
-  if (range.empty) {   // CTA-uniform: nothing in this split
-    leave_split<kOwn>(split, hkv, seq);
-    return;
-  }
-  const int t_begin = range.t_begin, t_end = range.t_end, skip = kOwn ? range.skip : 0;
+  const int raw_len = __ldg(a.seq_lens + seq);
+  const int len = clamp_len(raw_len, a);
+  if (raw_len != len && split == 0 && hkv == 0 && threadIdx.x == 0) atomicOr(a.status, kDevBadSeqLen);
+  const int split_tokens = a.split_pages * a.page_size;
+  const int t_begin = split * split_tokens;
+  if (t_begin >= len) return;  // CTA-uniform: nothing in this split
+  const int t_end = min(len, t_begin + split_tokens);
   const int n_chunks = (t_end - t_begin + kChunkTokens - 1) / kChunkTokens;
-  const int split_first_page = range.first_page;
+  const int split_first_page = split * a.split_pages;
   const int split_npages = (t_end - t_begin + a.page_size - 1) / a.page_size;
   const int pages_per_chunk = kChunkTokens / a.page_size;
 
@@ -573,8 +522,6 @@ __global__ void __launch_bounds__(kG4Threads, 2) decode_split_g4_kernel(const De
       }
       float sc = v[0];
       if (row_base + 2 * ph >= valid) sc = -INFINITY;
-      const int lo = (kOwn && c == 0) ? skip : 0;   // rows of the chunk before this carry no weight
-      if (kOwn && row_base + 2 * ph < lo) sc = -INFINITY;
       // ---- online softmax for head gh over the chunk's 4 rows of this segment
       float cm = fmaxf(sc, __shfl_xor_sync(seg_mask, sc, 4));
       cm = fmaxf(cm, __shfl_xor_sync(seg_mask, cm, 8));
@@ -599,7 +546,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) decode_split_g4_kernel(const De
       sp[lane_r] = pv;
       __syncwarp();
       // ---- acc += p * v for the 4 rows
-      if (valid == kChunkTokens && (!kOwn || lo == 0)) {
+      if (valid == kChunkTokens) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float4 w4 = *reinterpret_cast<const float4*>(sp + 4 * p);
@@ -619,7 +566,7 @@ __global__ void __launch_bounds__(kG4Threads, 2) decode_split_g4_kernel(const De
       } else {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          if (row_base + 2 * p < valid && (!kOwn || row_base + 2 * p >= lo)) {
+          if (row_base + 2 * p < valid) {
             const float4 w4 = *reinterpret_cast<const float4*>(sp + 4 * p);
             const uint4 vu = *reinterpret_cast<const uint4*>(sV + (row_base + 2 * p) * L::kRowBytes);
             const float2 v0 = bf16x2_to_f2(vu.x), v1 = bf16x2_to_f2(vu.y);
@@ -665,7 +612,6 @@ __global__ void __launch_bounds__(kG4Threads, 2) decode_split_g4_kernel(const De
         mbar_wait(FULL(cc % kDecStages), (cc / kDecStages) & 1u, nullptr, nullptr, kWaitLimitNs);
     }
     __syncthreads();
-    leave_split<kOwn>(split, hkv, seq);
     return;
   }
 
@@ -704,7 +650,6 @@ __global__ void __launch_bounds__(kG4Threads, 2) decode_split_g4_kernel(const De
     a.part_o[(row0 + static_cast<size_t>(g) * a.max_splits) * D + col] = o / tot;
     if (col == 0) a.part_lse[row0 + static_cast<size_t>(g) * a.max_splits] = fmaf(M, a.scale, __logf(tot));
   }
-  leave_split<kOwn>(split, hkv, seq);
 }
 
 template <int D>
@@ -828,72 +773,36 @@ static DecodeArgs make_args(const void* q, const void* k_cache, const void* v_ca
   a.part_o = plan ? reinterpret_cast<float*>(ws + plan->partial_o_offset) : nullptr;
   a.part_lse = plan ? reinterpret_cast<float*>(ws + plan->partial_lse_offset) : nullptr;
   a.status = status;
-  a.own_start = nullptr;
-  a.max_own = 0;
   return a;
 }
 
-// pdl: launched as a programmatic dependent of the kernel before it (own-keys form)
-template <typename Kernel>
-static cudaError_t launch_split_kernel(Kernel kernel, const DecodeArgs& a, dim3 grid, int threads, int smem, bool pdl,
-                                       cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
-template <int D, int G, bool kOwn>
-static cudaError_t launch_split(const DecodeArgs& a, dim3 grid, bool pdl, cudaStream_t stream) {
+template <int D, int G>
+static cudaError_t launch_split(const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   using L = DecodeLayout<D>;
   static int attr_done[64] = {0};
-  cudaError_t e = ensure_smem_limit(decode_split_kernel<D, G, kOwn>, L::kBytes, attr_done);
+  cudaError_t e = ensure_smem_limit(decode_split_kernel<D, G>, L::kBytes, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_split_kernel(decode_split_kernel<D, G, kOwn>, a, grid, kSplitThreads, L::kBytes, pdl, stream);
+  decode_split_kernel<D, G><<<grid, kSplitThreads, L::kBytes, stream>>>(a);
+  return cudaGetLastError();
 }
 
-template <bool kOwn>
-static cudaError_t launch_split_g4(const DecodeArgs& a, dim3 grid, bool pdl, cudaStream_t stream) {
+static cudaError_t launch_split_g4(const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   static int attr_done[64] = {0};
-  cudaError_t e = ensure_smem_limit(decode_split_g4_kernel<kOwn>, G4Layout::kBytes, attr_done);
+  cudaError_t e = ensure_smem_limit(decode_split_g4_kernel, G4Layout::kBytes, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_split_kernel(decode_split_g4_kernel<kOwn>, a, grid, kG4Threads, G4Layout::kBytes, pdl, stream);
+  decode_split_g4_kernel<<<grid, kG4Threads, G4Layout::kBytes, stream>>>(a);
+  return cudaGetLastError();
 }
 
-template <int D, bool kOwn>
-static cudaError_t launch_split_g(const DecodeArgs& a, int G, dim3 grid, bool pdl, cudaStream_t stream) {
-  if (D == 128 && G == 4) return launch_split_g4<kOwn>(a, grid, pdl, stream);
+template <int D>
+static cudaError_t launch_split_g(const DecodeArgs& a, int G, dim3 grid, cudaStream_t stream) {
+  if (D == 128 && G == 4) return launch_split_g4(a, grid, stream);
   switch (G) {
-    case 1: return launch_split<D, 1, kOwn>(a, grid, pdl, stream);
-    case 2: return launch_split<D, 2, kOwn>(a, grid, pdl, stream);
-    case 4: return launch_split<D, 4, kOwn>(a, grid, pdl, stream);
-    default: return launch_split<D, 8, kOwn>(a, grid, pdl, stream);
+    case 1: return launch_split<D, 1>(a, grid, stream);
+    case 2: return launch_split<D, 2>(a, grid, stream);
+    case 4: return launch_split<D, 4>(a, grid, stream);
+    default: return launch_split<D, 8>(a, grid, stream);
   }
-}
-
-// The own-keys half of the shared-prefix decode: splits of every sequence's
-// keys from own_start[s] on, partials as launch_paged_decode writes them.
-cudaError_t launch_decode_own(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                              const int32_t* seq_lens, const int32_t* own_start, int max_own, int page_size,
-                              int num_seqs, int Hq, int Hkv, int d, int max_pages, int num_pages_total, float scale,
-                              const DecodePlan& plan, float* part_o, float* part_lse, unsigned* status, bool pdl,
-                              cudaStream_t stream) {
-  DecodeArgs a = make_args(q, k_cache, v_cache, block_table, seq_lens, page_size, num_seqs, Hq, Hkv, max_pages,
-                           num_pages_total, scale, plan.split_pages, plan.max_splits, nullptr, nullptr, status);
-  a.part_o = part_o;
-  a.part_lse = part_lse;
-  a.own_start = own_start;
-  a.max_own = max_own;
-  const dim3 grid(plan.max_splits, Hkv, num_seqs);
-  return d == 128 ? launch_split_g<128, true>(a, Hq / Hkv, grid, pdl, stream)
-                  : launch_split_g<64, true>(a, Hq / Hkv, grid, pdl, stream);
 }
 
 ta_status launch_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -908,8 +817,7 @@ ta_status launch_paged_decode(const void* q, const void* k_cache, const void* v_
                            num_pages_total, scale, plan.split_pages, plan.max_splits, workspace, &plan, status);
   const int G = Hq / Hkv;
   dim3 grid(plan.max_splits, Hkv, num_seqs);
-  cudaError_t e = (d == 128) ? launch_split_g<128, false>(a, G, grid, false, stream)
-                             : launch_split_g<64, false>(a, G, grid, false, stream);
+  cudaError_t e = (d == 128) ? launch_split_g<128>(a, G, grid, stream) : launch_split_g<64>(a, G, grid, stream);
   if (e != cudaSuccess) return fail(TA_ERR_CUDA, "decode: split kernel launch", e);
   dim3 cgrid(Hq, num_seqs);
   if (d == 128)

@@ -7,28 +7,36 @@
 // alone reads every key once per sequence and is bound by those bytes.  Over a
 // shared prefix the queries of the whole group meet each key, so the prefix is
 // a matrix product: rows are (sequence, query head of one KV head) pairs, 128
-// to a tile, and K/V tiles of 128 keys are read once for up to 256 rows.
+// to a tile, and a K/V tile of 128 keys is read once for up to 256 rows.
 //
-// Four kernels, each a programmatic dependent of the one before where it can be:
+// Own keys run through the same tiles with Hq / Hkv rows of the 128 in use.
+// The waste is free: a 128-key tile of K and V is 64 KB, 1.5 us of one SM's
+// share of HBM, and its two products take 0.6 us of the tensor pipe however
+// many rows count, while the CUDA-core dot products of the paged decode are
+// bound by instructions at such short lengths (48 us here against 10 us of
+// bytes for 64 sequences of about 256 own tokens, 104 us against 8 us with
+// groups of 8 heads at d = 64).
+//
+// Three kernels, each a programmatic dependent of the one before:
 //   shared_plan_kernel     one CTA: the group of each sequence, where its own
-//                          keys start, and a running count of the prefix work
-//   prefix_kernel          tcgen05: all prefix work, cut evenly over the SMs
-//   decode_split_* <kOwn>  the paged decode's split kernels over own keys; they
-//                          fill SMs as prefix CTAs leave
+//                          keys start, and a running count of all the work
+//   shared_attend_kernel   all products, cut evenly over the SMs
 //   shared_combine_kernel  joins a row's partials by their log-sum-exp
 //
-// Work of the prefix kernel.  A unit is (group, KV head, 256 query rows); its
-// steps are the prefix's 128-key tiles.  All units' steps are laid end to end
-// and CTA c of n takes steps [c L, (c + 1) L), L = ceil(steps / n): equal shares
-// whatever the groups' sizes and lengths, at the price of one partial result
-// per CTA and unit it touches.  The (c, unit) pairs met along the line are
-// monotone in both, so slot c + unit holds a pair's partial without a table.
+// Work.  An item is a group's prefix or a sequence's own keys; a unit is (item,
+// KV head, block of 256 query rows); its steps are 128-key tiles.  All units'
+// steps are laid end to end, a step that serves more than 128 rows counting
+// kWideCost, others 1, and CTA c of n takes the steps that start in
+// [c L, (c + 1) L), L = ceil(total / n): equal shares whatever the groups' sizes
+// and lengths, at the price of partial results per CTA and unit it touches.
+// The (c, unit) pairs met along the line are monotone in both, so slot
+// c + unit holds a pair's partials without a table.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "ptx.cuh"
 #include "tiledattn_internal.h"
@@ -38,35 +46,68 @@ namespace {
 
 constexpr int kTile = 128;           // query rows and keys of a tile
 constexpr int kUnitRows = 2 * kTile;
-constexpr int kThreads = 384;
-constexpr int kSoftmaxWarp0 = 4;
-constexpr int kLaunchRegs = 168, kRegsControl = 56, kRegsSoftmax = 224;   // register split of the prefill kernel
-static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kLaunchRegs, "register split");
+// warp 0 plans, 1 and 12 issue the products of row tile 0 and 1, 2 copies queries and K, 3 copies V, 4-7 and 8-11 are
+// the softmax warpgroups of row tile 0 and 1
+constexpr int kThreads = 416;
+constexpr int kSoftmaxWarp0 = 4, kMmaWarp1 = 12;
 constexpr float kRescaleLog2 = 8.0f;   // the stale-max margin of the prefill kernel
-// Fewest steps a CTA takes.
-constexpr int kMinSteps = 1;
+constexpr int kWideShift = 1;          // a step with two row tiles costs 2^kWideShift, one with a single tile 1
+constexpr int kWideCost = 1 << kWideShift;
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// One group as the plan kernel found it: ranges checked, work counted.
-struct __align__(16) Group {
-  long long step0;   // steps of all groups before it
-  int unit0;         // units of all groups before it
-  int first, n;      // its sequences
-  int len;           // prefix length
-  int pad[2];
+// mbar_wait with its bounded loop out of line: the attend kernel waits at some
+// thirty places, and its roles share one instruction cache.
+__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, unsigned* status, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, status, abort_flag);
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, unsigned* status, volatile int* abort_flag) {
+  const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, status, abort_flag);
+  return __all_sync(0xffffffffu, ok);   // one answer for the warp
+}
+
+// Eight 32-bit columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Largest of a value over the warp (one instruction on sm_100a).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One group's prefix or one sequence's own keys, as the plan kernel found it:
+// ranges checked, work counted.
+struct __align__(16) Item {
+  long long x0;   // cost of all items before it
+  int unit0;      // units of its kind before it
+  int first, n;   // first sequence, number of sequences (own keys: 1)
+  int base;       // first key of its first tile (the start of a page)
+  int lo, end;    // its keys: [base + lo, end)
 };
-static_assert(sizeof(Group) == 32, "two 16-byte loads");
+static_assert(sizeof(Item) == 32, "two 16-byte loads");
 
 struct PlanHeader {
-  long long steps;     // of all groups
+  long long total;     // cost of all items
   long long per_cta;   // L
 };
 
-__host__ __device__ __forceinline__ int prefix_tiles(int len) { return (len + kTile - 1) / kTile; }
-__host__ __device__ __forceinline__ int row_blocks(int n, int G) {
-  return static_cast<int>((static_cast<long long>(n) * G + kUnitRows - 1) / kUnitRows);
+__host__ __device__ __forceinline__ int item_tiles(const Item& it) { return (it.end - it.base + kTile - 1) / kTile; }
+__host__ __device__ __forceinline__ int item_blocks(const Item& it, int G) {   // blocks of query rows
+  return static_cast<int>((static_cast<long long>(it.n) * G + kUnitRows - 1) / kUnitRows);
+}
+__host__ __device__ __forceinline__ int item_shift(const Item& it, int G) {   // log2 of the cost of one step
+  return it.n * G > kTile ? kWideShift : 0;
 }
 
 struct SharedArgs {
@@ -74,244 +115,303 @@ struct SharedArgs {
   const int32_t* seq_lens;
   const int32_t* group_offsets;
   const int32_t* prefix_lens;
-  int page_size, num_seqs, num_groups, Hq, Hkv, G, max_pages, num_pages_total, n_ctas;
-  int own_splits, own_split_pages, max_own;
+  int page_size, num_seqs, num_groups, Hq, Hkv, G, max_pages, num_pages_total, n_ctas, max_own;
   float scale, scale_log2;
   // workspace
   unsigned* status;
   PlanHeader* header;
-  Group* groups;        // [num_groups + 1]; the last only ends the counts
-  int32_t* own_start;   // [num_seqs] first key a sequence reads itself
-  int32_t* group_of;    // [num_seqs] group whose prefix it uses, or -1
+  Item* items;          // [num_groups + num_seqs + 1]: prefixes, own keys, the end of the line
+  int32_t* group_of;    // [num_seqs] group whose prefix a sequence uses, or -1
   float* pre_o;         // [slots][D / 4][256][4] normalised prefix partials
   float* pre_lse;       // [slots][256]
-  float* own_o;         // [num_seqs][Hq][own_splits][D]
-  float* own_lse;       // [num_seqs][Hq][own_splits]
+  float* own_o;         // [slots][2][G][D] normalised partials of own keys
+  float* own_lse;       // [slots][2][G]
 };
 
 // ---------------------------------------------------------------------------
 // Plan
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
+constexpr int kStagedGroups = 1024;   // group offsets held in shared memory
 
-// bad_offsets: the offsets decrease or leave the batch, so groups might overlap.
-__device__ __forceinline__ Group read_group(const SharedArgs& a, int g, bool& bad_offsets, bool& bad_len) {
+// A group's prefix with its ranges checked.  bad_offsets: the offsets decrease
+// or leave the batch, so groups might overlap.
+__device__ __forceinline__ Item read_group(const SharedArgs& a, int g, bool& bad_offsets, bool& bad_len) {
   const int cap = a.max_pages * a.page_size;
   const int lo = __ldg(a.group_offsets + g), hi = __ldg(a.group_offsets + g + 1), len = __ldg(a.prefix_lens + g);
-  Group r = {};
+  Item r = {};
   r.first = min(max(lo, 0), a.num_seqs);
-  const int end = min(max(hi, r.first), a.num_seqs);
-  r.n = end - r.first;
-  r.len = r.n > 0 ? min(max(len, 0), cap) : 0;   // a group without sequences shares nothing, whatever its length
-  bad_offsets = bad_offsets || lo != r.first || hi != end;
-  bad_len = bad_len || (r.n > 0 && len != r.len);
+  const int last = min(max(hi, r.first), a.num_seqs);
+  r.n = last - r.first;
+  r.end = r.n > 0 ? min(max(len, 0), cap) : 0;   // a group without sequences shares nothing, whatever its length
+  bad_offsets = bad_offsets || lo != r.first || hi != last;
+  bad_len = bad_len || (r.n > 0 && len != r.end);
   return r;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
-  __shared__ long long s_steps[kPlanThreads / 32];
-  __shared__ int s_units[kPlanThreads / 32];
-  grid_launch_dependents();   // the prefix kernel sets up meanwhile; it waits before it reads the plan
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) *a.status = 0;
-  __syncthreads();
-  bool bad_offsets = false, bad_len = false, seen = false;
-
-  // running counts over the groups: each thread a contiguous run of them
-  const int run = (a.num_groups + kPlanThreads - 1) / kPlanThreads;
-  const int g0 = min(tid * run, a.num_groups), g1 = min(g0 + run, a.num_groups);
-  long long steps = 0;
-  int units = 0;
-  auto group_units = [&](const Group& r) { return r.len > 0 ? row_blocks(r.n, a.G) * a.Hkv : 0; };
-  for (int g = g0; g < g1; ++g) {
-    const Group r = read_group(a, g, bad_offsets, bad_len);
-    const int u = group_units(r);
-    units += u;
-    steps += static_cast<long long>(u) * prefix_tiles(r.len);
-  }
-  long long st = steps;
-  int un = units;
+// Sums over the threads before this one (`before`), and over all (`total`).
+__device__ __forceinline__ void block_scan(long long v, int u, long long& before, int& before_u, long long& total) {
+  __shared__ long long s_v[kPlanThreads / 32];
+  __shared__ int s_u[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long sv = v;
+  int su = u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, st, o);
-    const int y = __shfl_up_sync(0xffffffffu, un, o);
+    const long long x = __shfl_up_sync(0xffffffffu, sv, o);
+    const int y = __shfl_up_sync(0xffffffffu, su, o);
     if (lane >= o) {
-      st += x;
-      un += y;
+      sv += x;
+      su += y;
     }
   }
+  __syncthreads();   // an earlier scan's sums have been read
   if (lane == 31) {
-    s_steps[warp] = st;
-    s_units[warp] = un;
+    s_v[warp] = sv;
+    s_u[warp] = su;
   }
-  // groups that might overlap are all left out (flagged): every sequence then reads its own keys only
-  const bool ignore = __syncthreads_or(bad_offsets);
-  long long before = st - steps, total = 0;
-  int before_u = un - units;
+  __syncthreads();
+  before = sv - v;
+  before_u = su - u;
+  total = 0;
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < warp) {
-      before += s_steps[w];
-      before_u += s_units[w];
+      before += s_v[w];
+      before_u += s_u[w];
     }
-    total += s_steps[w];
+    total += s_v[w];
   }
-  for (int g = g0; g < g1; ++g) {
-    Group r = read_group(a, g, seen, seen);
-    r.step0 = before;
-    r.unit0 = before_u;
-    a.groups[g] = r;
-    const int u = group_units(r);
-    before_u += u;
-    before += static_cast<long long>(u) * prefix_tiles(r.len);
-  }
-  if (ignore) total = 0;
-  if (tid == 0) {
-    Group end = {};
-    end.step0 = total;
-    a.groups[a.num_groups] = end;
-    a.header->steps = total;
-    const long long per = (total + a.n_ctas - 1) / a.n_ctas;
-    a.header->per_cta = per < kMinSteps ? kMinSteps : per;
-  }
+}
 
-  // The group of each sequence: the first whose end lies behind it.  A
-  // sequence shorter than its group's prefix does not use it (its keys are
-  // all its own).
-  for (int s = tid; s < a.num_seqs; s += kPlanThreads) {
-    int lo = 0, hi = a.num_groups;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.group_offsets + mid + 1) <= s) lo = mid + 1;
-      else hi = mid;
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
+  __shared__ int s_off[kStagedGroups + 1];
+  grid_launch_dependents();   // the attend kernel sets up meanwhile; it waits before it reads the plan
+  const int tid = threadIdx.x;
+  if (tid == 0) *a.status = 0;
+  const bool staged = a.num_groups <= kStagedGroups;
+  if (staged && a.num_groups > 0)
+    for (int g = tid; g <= a.num_groups; g += kPlanThreads) s_off[g] = __ldg(a.group_offsets + g);
+  bool bad_offsets = false, bad_len = false, seen = false;
+
+  // prefixes: each thread a contiguous run of groups
+  long long total = 0;
+  bool ignore = false;
+  if (a.num_groups > 0) {
+    const int run = (a.num_groups + kPlanThreads - 1) / kPlanThreads;
+    const int g0 = min(tid * run, a.num_groups), g1 = min(g0 + run, a.num_groups);
+    auto units_of = [&](const Item& r) { return r.end > 0 ? item_blocks(r, a.G) * a.Hkv : 0; };
+    auto cost_of = [&](const Item& r) { return (static_cast<long long>(units_of(r)) * item_tiles(r)) << item_shift(r, a.G); };
+    long long cost = 0, before;
+    int units = 0, before_u;
+    for (int g = g0; g < g1; ++g) {
+      const Item r = read_group(a, g, bad_offsets, bad_len);
+      units += units_of(r);
+      cost += cost_of(r);
     }
-    int start = 0, of = -1;
-    if (lo < a.num_groups && !ignore) {
-      const Group r = read_group(a, lo, seen, seen);
-      if (s >= r.first && s < r.first + r.n && r.len > 0 && __ldg(a.seq_lens + s) >= r.len) {
-        start = r.len;
-        of = lo;
+    // groups that might overlap are all left out (flagged): every sequence then reads its own row only
+    ignore = __syncthreads_or(bad_offsets);
+    block_scan(cost, units, before, before_u, total);
+    for (int g = g0; g < g1; ++g) {
+      Item r = read_group(a, g, seen, seen);
+      r.x0 = ignore ? 0 : before;
+      r.unit0 = before_u;
+      a.items[g] = r;
+      before += cost_of(r);
+      before_u += units_of(r);
+    }
+    if (ignore) total = 0;
+  }
+  __syncthreads();
+
+  // own keys: each thread a contiguous run of sequences.  A sequence shorter
+  // than its group's prefix does not use it (all its keys are its own).
+  const int run = (a.num_seqs + kPlanThreads - 1) / kPlanThreads;
+  const int s0 = min(tid * run, a.num_seqs), s1 = min(s0 + run, a.num_seqs);
+  const int cap = a.max_pages * a.page_size;
+  auto own_keys = [&](int s, int& of) {
+    const int raw = __ldg(a.seq_lens + s);
+    int len = min(max(raw, 0), cap), start = 0;
+    of = -1;
+    if (!ignore) {   // the first group whose end lies behind it
+      int lo = 0, hi = a.num_groups;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((staged ? s_off[mid + 1] : __ldg(a.group_offsets + mid + 1)) <= s) lo = mid + 1;
+        else hi = mid;
+      }
+      if (lo < a.num_groups && (staged ? s_off[lo] : __ldg(a.group_offsets + lo)) <= s) {
+        const int prefix = min(max(__ldg(a.prefix_lens + lo), 0), cap);
+        if (prefix > 0 && len >= prefix) {
+          start = prefix;
+          of = lo;
+        }
       }
     }
-    a.own_start[s] = start;
+    if (raw != len || len - start > a.max_own) bad_len = true;
+    len = min(len, start + a.max_own);
+    Item r = {};
+    r.unit0 = s * a.Hkv;
+    r.first = s;
+    r.n = 1;
+    r.base = start / a.page_size * a.page_size;
+    r.lo = start - r.base;
+    r.end = len > start ? len : r.base;   // no key of its own: no tile
+    return r;
+  };
+  long long cost = 0, before, own_total;
+  int unused, of;
+  for (int s = s0; s < s1; ++s) cost += static_cast<long long>(item_tiles(own_keys(s, of))) * a.Hkv;
+  block_scan(cost, 0, before, unused, own_total);
+  before += total;
+  for (int s = s0; s < s1; ++s) {
+    Item r = own_keys(s, of);
+    r.x0 = before;
+    a.items[a.num_groups + s] = r;
     a.group_of[s] = of;
+    before += static_cast<long long>(item_tiles(r)) * a.Hkv;
+  }
+  total += own_total;
+  if (tid == 0) {
+    Item end = {};
+    end.x0 = total;
+    a.items[a.num_groups + a.num_seqs] = end;
+    a.header->total = total;
+    const long long per = (total + a.n_ctas - 1) / a.n_ctas;
+    a.header->per_cta = per < kWideCost ? kWideCost : per;   // a share holds the start of at least one step of any unit inside it
   }
   if (bad_offsets || bad_len) atomicOr(a.status, kDevBadSeqLen);
 }
 
+// Steps of a unit that start in CTA c's share: [j0, j1) of `tiles`, x0 the
+// unit's place on the line, 2^shift the cost of a step.
+__device__ __forceinline__ void unit_share(long long x0, int tiles, int shift, long long per, int c, int& j0, int& j1) {
+  const long long a = per * c - x0, b = a + per, up = (1 << shift) - 1;
+  j0 = a <= 0 ? 0 : static_cast<int>((a + up) >> shift);
+  const long long e = (b + up) >> shift;
+  j1 = e < tiles ? static_cast<int>(e) : tiles;
+}
+
 // ---------------------------------------------------------------------------
-// Prefix
+// Attend
 // ---------------------------------------------------------------------------
+// A segment: the steps of one unit that one CTA takes.  The producer describes
+// each to the other roles through a ring in shared memory.  Rows up to 128
+// ("narrow"): steps alternate between the two row tiles of the CTA, which both
+// hold the same query rows, so two softmax warpgroups work on two key tiles at
+// once; each tile's steps give a partial of their own.  More rows ("wide"):
+// both tiles take every step, each with its own rows.
+struct __align__(16) Segment {
+  uint32_t g0;     // ring position of its first key tile
+  int tiles;       // steps; 0 ends the work
+  int wide;        // 1: two row tiles in every step
+  int tile_first;  // narrow: the row tile of step 0
+  int rows;        // query rows of the unit (1..256)
+  int lo, hi;      // keys, counted from its first key tile: [lo, hi)
+  int slot;        // of its partials: >= 0 prefix, ~slot own keys
+  int hkv, seq;    // KV head, first sequence of the query rows
+  int row, page0;  // block-table row, its first page
+  int qslot, pad[3];      // own keys: where in the query buffers its rows are (in 8 rows)
+  int pages[kTile / 8];   // physical pages of its first key tile, -1 past the keys
+};
+static_assert(sizeof(Segment) == 128, "16-byte loads");
+constexpr int kSegments = 4;   // ring depth
+// Query loads of a row tile that may be outstanding: a segment is described
+// only when the one kSegments before it has been taken up by every role, so
+// more than kSegments of them cannot be.
+constexpr uint32_t kQLoads = 8;
+// Own keys have at most 8 query rows.  Their loads go round 8 places of 8 rows in
+// the first half of a query buffer, so the loads of the next segments need not
+// wait for the products of this one; the second half takes the weights of the
+// step (prefixes come first on the line, so no whole query tile follows).
+constexpr int kQSlots = 8, kOwnP = 64 * 128;
+constexpr int kOwnCols = 16;   // columns of the own-keys products: 8 rows of queries, and 8 that do not count
+
 template <int D>
-struct PrefixLayout {
+struct AttendLayout {
   static constexpr int kChunks = D / 64;               // 128-byte swizzle rows along d
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kChunkBytes = kTile * 128;
-  static constexpr int kStages = D == 128 ? 2 : 4;     // K ring and V ring depth
+  // ring depths: K tiles are free once their scores are formed, V tiles only
+  // after the softmax, so V gets the one that is left of 227 KB
+  static constexpr int kKStages = D == 128 ? 2 : 4, kVStages = D == 128 ? 3 : 6;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + 2 * kTileBytes;
-  static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kBar = kV + kStages * kTileBytes;
-  // q, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_ready[2], o_done[2], p_half[2],
-  // q_free, o_free[2], mma_done
-  static constexpr int kNumBars = 1 + 4 * kStages + 12;
+  static constexpr int kV = kK + kKStages * kTileBytes;
+  static constexpr int kSeg = kV + kVStages * kTileBytes;
+  static constexpr int kRed = kSeg + kSegments * static_cast<int>(sizeof(Segment));   // [row tile][2][4 warps][8] floats
+  static constexpr int kBar = kRed + 2 * 2 * 4 * 8 * 4;
+  // k_full, k_empty, v_full, v_empty; per row tile: s_full, p_half, p_ready, o_free, o_done, exchange, q_full[]; segment full, empty;
+  // mma_done
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 12 + 2 * kQLoads + 2 * kSegments + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag
-  static constexpr int kAlloc = kMisc + 16 + 1024;      // slack to align the base to 1024 B
+  // slack to align the base to 1024 B; with d = 64 the own-keys product reads 64 rows it does not need, 1 KB on
+  static constexpr int kAlloc = kMisc + 16 + 1024 + (D == 64 ? 1024 : 0);
+  static_assert(kAlloc <= 232448, "shared memory of one CTA");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kTmS0 = 0, kTmS1 = 128, kTmO0 = 256, kTmO1 = 256 + D;
 };
 
-// The CTA's place on the line of steps.  All roles walk it alike.
-struct Segment {
-  int row0;          // first row of the unit among the group's (sequence, head) rows
-  int rows;          // rows of the unit (1..256)
-  int first;         // first sequence of the group
-  int hkv, len;      // KV head, prefix length
-  int tile0, tiles;  // key tiles [tile0, tile0 + tiles)
-  int slot;          // of its partial result
-};
-struct Walk {   // groups are read again for each segment: registers are scarcer than cached loads
-  long long x, end;
-  int g;
-
-  __device__ __forceinline__ void start(const SharedArgs& a, long long steps, long long per) {
-    x = per * blockIdx.x;
-    end = min(steps, x + per);
-    int lo = 0, hi = a.num_groups;   // the last group that starts at or before x: it owns step x
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.groups[mid].step0 <= x) lo = mid;
-      else hi = mid;
-    }
-    g = lo;
-  }
-  __device__ __forceinline__ bool more() const { return x < end; }
-  __device__ __forceinline__ Segment next(const SharedArgs& a) {
-    while (a.groups[g + 1].step0 <= x) ++g;   // the entry behind the last group holds the total
-    const Group grp = a.groups[g];
-    const int tiles = prefix_tiles(grp.len), blocks = row_blocks(grp.n, a.G);
-    const long long in_group = x - grp.step0, unit = in_group / tiles;
-    Segment s;
-    s.tile0 = static_cast<int>(in_group - unit * tiles);
-    s.tiles = static_cast<int>(min(static_cast<long long>(tiles - s.tile0), end - x));
-    s.hkv = static_cast<int>(unit) / blocks;
-    s.row0 = static_cast<int>(unit) % blocks * kUnitRows;
-    s.rows = min(kUnitRows, grp.n * a.G - s.row0);
-    s.first = grp.first;
-    s.len = grp.len;
-    s.slot = static_cast<int>(blockIdx.x) + grp.unit0 + static_cast<int>(unit);
-    x += s.tiles;
-    return s;
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
-  using L = PrefixLayout<D>;
+    shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const SharedArgs a) {
+  using L = AttendLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
-  const uint32_t bar0 = sbase + L::kBar;
-  constexpr int S4 = 4 * L::kStages;
-  const uint32_t BAR_Q = bar0, BAR_QE = bar0 + 8u * (9 + S4), BAR_FIN = bar0 + 8u * (12 + S4);
-  auto BAR_KF = [&](int s) { return bar0 + 8u * (1 + s); };
-  auto BAR_KE = [&](int s) { return bar0 + 8u * (1 + L::kStages + s); };
-  auto BAR_VF = [&](int s) { return bar0 + 8u * (1 + 2 * L::kStages + s); };
-  auto BAR_VE = [&](int s) { return bar0 + 8u * (1 + 3 * L::kStages + s); };
-  auto BAR_SF = [&](int t) { return bar0 + 8u * (1 + S4 + t); };
-  auto BAR_PR = [&](int t) { return bar0 + 8u * (3 + S4 + t); };
-  auto BAR_OD = [&](int t) { return bar0 + 8u * (5 + S4 + t); };
-  auto BAR_PH = [&](int t) { return bar0 + 8u * (7 + S4 + t); };
-  auto BAR_OF = [&](int t) { return bar0 + 8u * (10 + S4 + t); };
+  constexpr uint32_t KS = L::kKStages, VS = L::kVStages;
+  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (12 + 2 * kQLoads);
+  auto BAR_KF = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto BAR_KE = [&](uint32_t s) { return bar0 + 8u * (KS + s); };
+  auto BAR_VF = [&](uint32_t s) { return bar0 + 8u * (2 * KS + s); };
+  auto BAR_VE = [&](uint32_t s) { return bar0 + 8u * (2 * KS + VS + s); };
+  auto BAR_SF = [&](int t) { return bar_t + 8u * t; };
+  auto BAR_PH = [&](int t) { return bar_t + 8u * (2 + t); };
+  auto BAR_PR = [&](int t) { return bar_t + 8u * (4 + t); };
+  auto BAR_OF = [&](int t) { return bar_t + 8u * (6 + t); };
+  auto BAR_OD = [&](int t) { return bar_t + 8u * (8 + t); };
+  auto BAR_X = [&](int t) { return bar_t + 8u * (10 + t); };
+  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (12 + t * kQLoads + load % kQLoads); };
+  auto BAR_GF = [&](uint32_t e) { return bar_s + 8u * e; };
+  auto BAR_GE = [&](uint32_t e) { return bar_s + 8u * (kSegments + e); };
+  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments;
+  Segment* ring = reinterpret_cast<Segment*>(smem + L::kSeg);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- setup, before the plan is needed
   if (threadIdx.x == 0) {
-    mbar_init(BAR_Q, 1);
-    for (int s = 0; s < L::kStages; ++s) {
+    for (uint32_t s = 0; s < KS; ++s) {
       mbar_init(BAR_KF(s), 1);
-      mbar_init(BAR_KE(s), 1);
+      mbar_init(BAR_KE(s), 2);   // both row tiles' warps (narrow: twice by the one that takes the step)
+    }
+    for (uint32_t s = 0; s < VS; ++s) {
       mbar_init(BAR_VF(s), 1);
-      mbar_init(BAR_VE(s), 1);
+      mbar_init(BAR_VE(s), 2);
     }
     for (int t = 0; t < 2; ++t) {
+      for (uint32_t u = 0; u < kQLoads; ++u) mbar_init(BAR_QF(t, u), 1);
       mbar_init(BAR_SF(t), 1);
-      mbar_init(BAR_PR(t), 128);
-      mbar_init(BAR_OD(t), 1);
       mbar_init(BAR_PH(t), 128);
+      mbar_init(BAR_PR(t), 128);
       mbar_init(BAR_OF(t), 128);
+      mbar_init(BAR_OD(t), 1);
+      mbar_init(BAR_X(t), 4);   // one lane of each softmax warp
     }
-    mbar_init(BAR_QE, 1);
-    mbar_init(BAR_FIN, 1);
+    for (uint32_t e = 0; e < kSegments; ++e) {
+      mbar_init(BAR_GF(e), 1);
+      mbar_init(BAR_GE(e), 4 + 256);   // the MMA and copying warps and every softmax thread
+    }
+    mbar_init(BAR_FIN, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmQ1);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
@@ -324,272 +424,531 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  grid_wait();                // the plan is complete
-  grid_launch_dependents();   // the own-keys kernel may take the SMs this grid leaves
-  const long long steps = a.header->steps, per = a.header->per_cta;
-  Walk walk;
-  walk.start(a, steps, per);
-
-  if (warp < kSoftmaxWarp0) {
-    setmaxnreg_dec<kRegsControl>();
+  if (warp < kSoftmaxWarp0 || warp == kMmaWarp1) {
     if (warp == 0) {
-      // ======================= TMA producer (lane p: page p of a tile) =======================
-      const int per_tile = kTile / a.page_size;
-      const uint32_t page_bytes = static_cast<uint32_t>(a.page_size) * D * 2;
-      bool ok = true;
-      uint32_t g = 0, gv = 0;    // K and V tiles whose copies were issued
-      int qi = 0;
-      while (walk.more() && ok) {
-        const Segment sg = walk.next(a);
-        const int32_t* row = a.block_table + static_cast<size_t>(sg.first) * a.max_pages;
-        // this lane's page of key tile j, -1 past the prefix; an entry outside the pool reads page 0 and is flagged
-        auto page_of = [&](int j) {
-          const int p = j * per_tile + lane;
-          if (lane >= per_tile || static_cast<long long>(p) * a.page_size >= sg.len) return -1;
-          int pg = __ldg(row + p);
-          if (pg < 0 || pg >= a.num_pages_total) {
+      // ======================= planner: describes the CTA's segments, up to kSegments ahead =======================
+      grid_wait();                // the plan is complete
+      grid_launch_dependents();
+      const long long per = a.header->per_cta;
+      const long long begin = per * blockIdx.x, end = min(a.header->total, begin + per);
+      const int n_items = a.num_groups + a.num_seqs, per_tile = kTile / a.page_size;
+      // where the walk is: item, unit of it, and the unit's place on the line
+      int item = 0, unit = 0, tiles = 0, blocks = 1, shift = 0;
+      long long ux = 0;
+      Item it = {};
+      auto enter = [&](int at) {   // the first item from `at` on that has work
+        for (item = at; item < n_items; ++item) {
+          it = a.items[item];
+          tiles = item_tiles(it);
+          if (tiles > 0 && it.n > 0 && a.items[item + 1].x0 > it.x0) break;
+        }
+        blocks = item_blocks(it, a.G);
+        shift = item_shift(it, a.G);
+        unit = 0;
+        ux = it.x0;
+      };
+      if (begin < end) {   // the last item that starts at or before `begin` owns it: a 32-way search
+        int lo = 0, n = n_items;
+        while (n > 1) {
+          const int step = (n + 31) / 32, at = lane * step;
+          const uint32_t le = __ballot_sync(0xffffffffu, at < n && a.items[lo + at].x0 <= begin);
+          const int k = 31 - __clz(le);   // items start in order, and the first does at or before `begin`
+          lo += k * step;
+          n = min(step, n - k * step);
+        }
+        enter(lo);
+        const long long unit_cost = static_cast<long long>(tiles) << shift;
+        unit = static_cast<int>((begin - ux) / unit_cost);
+        ux += unit * unit_cost;
+      } else {
+        ux = end;
+      }
+      auto advance = [&]() {   // to the next unit, if the share reaches it
+        ux += static_cast<long long>(tiles) << shift;
+        if (ux < end && ++unit == blocks * a.Hkv) enter(item + 1);
+      };
+      uint32_t g0 = 0;
+      int turn = 0;   // row tile that takes the next narrow step
+      for (uint32_t n = 0;; ++n) {
+        int j0 = 0, j1 = 0;
+        while (ux < end) {
+          unit_share(ux, tiles, shift, per, static_cast<int>(blockIdx.x), j0, j1);
+          if (j0 < j1) break;   // else the share begins inside the unit's last step
+          advance();
+        }
+        const bool done = j0 >= j1;
+        Segment sg = {};
+        int pg = -1;
+        if (!done) {
+          const int row0 = unit % blocks * kUnitRows;
+          const bool own = item >= a.num_groups;
+          sg.g0 = g0;
+          sg.tiles = j1 - j0;
+          sg.rows = min(kUnitRows, it.n * a.G - row0);
+          sg.wide = sg.rows > kTile;
+          sg.tile_first = turn;
+          sg.lo = j0 == 0 ? it.lo : 0;
+          sg.hi = it.end - it.base - j0 * kTile;
+          const int slot = static_cast<int>(blockIdx.x) + it.unit0 + unit;
+          sg.slot = own ? ~slot : slot;
+          sg.hkv = unit / blocks;
+          sg.seq = it.first + row0 / a.G;
+          sg.row = it.first;
+          sg.page0 = it.base / a.page_size + j0 * per_tile;
+          sg.qslot = own ? static_cast<int>(n % kQSlots) : 0;
+          g0 += sg.tiles;
+          if (!sg.wide) turn ^= sg.tiles & 1;
+          const bool mine = lane < per_tile && lane * a.page_size < sg.hi;
+          if (mine) pg = __ldg(a.block_table + static_cast<size_t>(sg.row) * a.max_pages + sg.page0 + lane);
+          advance();   // while the table entries are under way
+          if (mine && (pg < 0 || pg >= a.num_pages_total)) {   // read as page 0, flagged
             atomicOr(a.status, kDevBadBlockTable);
             pg = 0;
           }
-          return pg;
-        };
-        int pg = page_of(sg.tile0);
-        if (qi > 0 && !(ok = mbar_wait_warp(BAR_QE, static_cast<uint32_t>(qi - 1) & 1u, a.status, abort_flag))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(BAR_Q, (sg.rows > kTile ? 2u : 1u) * L::kTileBytes);
-          const int seq0 = sg.first + sg.row0 / a.G, seqs = kTile / a.G;
-          tma_load_4d(sQ, &tmQ, BAR_Q, 0, sg.hkv * a.G, seq0, 0);
-          if (sg.rows > kTile) tma_load_4d(sQ + L::kTileBytes, &tmQ, BAR_Q, 0, sg.hkv * a.G, seq0 + seqs, 0);
         }
-        ++qi;
-        // A page arrives in one copy, in the layouts of the paged prefill: with two
-        // 64-column chunks K in the 32-byte swizzle ([8-row group][K step][8 rows]
-        // [32 B]) and V page-major ([page][chunk][page rows][128 B]).
-        auto copy = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, bool is_v) {
+        const uint32_t e = n % kSegments;
+        if (n >= kSegments && !wait_all(BAR_GE(e), (n / kSegments - 1) & 1u, a.status, abort_flag)) break;
+        if (lane < kTile / 8) ring[e].pages[lane] = pg;
+        if (lane == 0) {
+          const int4* src = reinterpret_cast<const int4*>(&sg);
+          int4* dst = reinterpret_cast<int4*>(&ring[e]);
+          dst[0] = src[0];
+          dst[1] = src[1];
+          dst[2] = src[2];
+          dst[3] = src[3];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR_GF(e));
+        if (done) break;
+      }
+    } else if (warp == 2 || warp == 3) {
+      // ======================= copying warps: 2 queries and K, 3 V (lane p: page p of a key tile) =======================
+      const bool is_v = warp == 3;
+      const int per_tile = kTile / a.page_size;
+      const uint32_t page_bytes = static_cast<uint32_t>(a.page_size) * D * 2;
+      const uint32_t stages = is_v ? VS : KS, data = is_v ? sV : sK;
+      const uint32_t full0 = is_v ? BAR_VF(0) : BAR_KF(0), empty0 = is_v ? BAR_VE(0) : BAR_KE(0);
+      const CUtensorMap* tm = is_v ? &tmV : &tmK;
+      uint32_t slot = 0, use = 0;   // ring slot of the next tile, and how often the ring went round
+      uint32_t qn[2] = {0, 0};      // loads into each query buffer
+      uint32_t qlast[2] = {0, 0};   // ring position of the last step that reads each
+      bool qown[2] = {false, false};
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const uint32_t e = n % kSegments;
+        if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, a.status, abort_flag))) break;
+        const Segment& sg = ring[e];
+        const int tiles = sg.tiles, hkv = sg.hkv, hi = sg.hi, seq = sg.seq, wide = sg.wide, tile_first = sg.tile_first;
+        const uint32_t g0 = sg.g0;
+        const bool own = sg.slot < 0;
+        const uint32_t qoff = static_cast<uint32_t>(sg.qslot) * 1024u;
+        const int32_t* row = a.block_table + static_cast<size_t>(sg.row) * a.max_pages + sg.page0;
+        int pg = lane < kTile / 8 ? sg.pages[lane] : -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR_GE(e));
+        if (tiles == 0) break;
+        // queries: narrow segments of several steps keep the same rows in both buffers
+        for (int t = 0; t < 2 && !is_v; ++t) {
+          if (!wide && tiles == 1 && t != tile_first) continue;
+          // A whole tile, or rows after one, wait until the scores of the last step that reads the buffer are formed:
+          // where that step's K slot has not been waited for since, its release says so.
+          if (qn[t] > 0 && !(own && qown[t]) && qlast[t] + KS >= g0 &&
+              !(ok = wait_all(BAR_KE(qlast[t] % KS), (qlast[t] / KS) & 1u, a.status, abort_flag)))
+            break;
+          const uint32_t bar = BAR_QF(t, qn[t]);
+          ++qn[t];
+          const int last = wide ? tiles - 1 : tiles - 1 - ((tile_first + tiles - 1 + t) & 1);
+          qlast[t] = g0 + static_cast<uint32_t>(last);
+          qown[t] = own;
+          if (lane == 0) {
+            const uint32_t dst = sQ + t * L::kTileBytes + qoff;
+            if (own) {   // one sequence: its G rows
+              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.G) * D * 2);
+              for (int c = 0; c < L::kChunks; ++c)
+                tma_load_4d(dst + c * L::kChunkBytes, &tmQ1, bar, 0, hkv * a.G, seq, c);
+            } else {
+              mbar_arrive_expect_tx(bar, L::kTileBytes);
+              tma_load_4d(dst, &tmQ, bar, 0, hkv * a.G, seq + (wide ? t * (kTile / a.G) : 0), 0);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        // key tiles.  A page arrives in one copy in the 128-byte swizzle: K as [8-row
+        // group][64-column chunk][8 rows][128 B], V as [chunk][page rows][128 B].
+        for (int j = 0; j < tiles; ++j) {
+          int pg_next = -1;   // under way before the wait
+          const int p = (j + 1) * per_tile + lane;
+          const bool more = j + 1 < tiles && lane < per_tile && static_cast<long long>(p) * a.page_size < hi;
+          if (more) pg_next = __ldg(row + p);
+          if (!(ok = wait_all(empty0 + 8u * slot, (use & 1u) ^ 1u, a.status, abort_flag))) break;
+          const uint32_t bar = full0 + 8u * slot;
           const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(live)) * page_bytes);
           __syncwarp();
           if (pg >= 0) {
-            const uint32_t at = dst + static_cast<uint32_t>(lane) * page_bytes;
-            if (L::kChunks == 1) tma_load_4d(at, tm, bar, 0, 0, sg.hkv, pg);
-            else if (is_v) tma_load_5d(at, tm, bar, 0, 0, 0, sg.hkv, pg);
-            else tma_load_5d(at, tm, bar, 0, 0, 0, 0, pg * a.Hkv + sg.hkv);
+            const uint32_t at = data + slot * L::kTileBytes + static_cast<uint32_t>(lane) * page_bytes;
+            tma_load_5d(at, tm, bar, 0, 0, 0, is_v ? hkv : 0, is_v ? pg : pg * a.Hkv + hkv);
           }
-        };
-        for (int j = 0; j < sg.tiles; ++j) {
-          const int s = static_cast<int>(g % L::kStages);
-          const uint32_t ph = (g / L::kStages) & 1u;
-          if (!(ok = mbar_wait_warp(BAR_KE(s), ph ^ 1u, a.status, abort_flag))) break;
-          copy(&tmK, sK + s * L::kTileBytes, BAR_KF(s), false);
-          ++g;
-          if (!(ok = mbar_wait_warp(BAR_VE(s), ph ^ 1u, a.status, abort_flag))) break;
-          copy(&tmV, sV + s * L::kTileBytes, BAR_VF(s), true);
-          ++gv;
-          if (j + 1 < sg.tiles) pg = page_of(sg.tile0 + j + 1);
+          if (++slot == stages) {
+            slot = 0;
+            ++use;
+          }
+          if (more && (pg_next < 0 || pg_next >= a.num_pages_total)) {   // read as page 0, flagged
+            atomicOr(a.status, kDevBadBlockTable);
+            pg_next = 0;
+          }
+          pg = pg_next;
         }
       }
       // drain: no copy into this CTA's shared memory may still be in flight at exit
       if (lane == 0) {
-        if (qi > 0) mbar_wait(BAR_Q, static_cast<uint32_t>(qi - 1) & 1u, nullptr, nullptr, kWaitLimitNs);
-        constexpr uint32_t kS = L::kStages;
-        for (uint32_t gg = (g > kS ? g - kS : 0u); gg < g; ++gg)
-          mbar_wait(BAR_KF(static_cast<int>(gg % kS)), (gg / kS) & 1u, nullptr, nullptr, kWaitLimitNs);
-        for (uint32_t gg = (gv > kS ? gv - kS : 0u); gg < gv; ++gg)
-          mbar_wait(BAR_VF(static_cast<int>(gg % kS)), (gg / kS) & 1u, nullptr, nullptr, kWaitLimitNs);
+        for (int t = 0; t < 2; ++t)
+          for (uint32_t u = qn[t] > kQLoads ? qn[t] - kQLoads : 0u; u < qn[t]; ++u)
+            mbar_wait(BAR_QF(t, u), (u / kQLoads) & 1u, nullptr, nullptr, kWaitLimitNs);
+        for (uint32_t k = 0; k < stages; ++k)   // the last fill of each slot
+          if (use > 0 || k < slot)
+            mbar_wait(full0 + 8u * k, (k < slot ? use : use - 1) & 1u, nullptr, nullptr, kWaitLimitNs);
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // ======================= MMA issuer (whole warp; the elected lane issues) =======================
+    } else {
+      // ======================= MMA issuers, one warp per row tile (whole warp; the elected lane issues) ===========
+      // Each tile's chain - scores, softmax, product with V, next scores - is a
+      // string of waits and issues of some hundred cycles each; from one warp the
+      // two tiles' chains add up (a narrow step took 2.4 us), from two they overlap.
+      const int t = warp == kMmaWarp1 ? 1 : 0;
       const bool leader = elect_one_sync();
       constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kTile, D, true);
-      auto commit = [&](uint32_t bar) {
-        if (leader) mma_commit(bar);
-        __syncwarp();
-      };
-      auto tS = [&](int t) { return tmem + (t ? L::kTmS1 : L::kTmS0); };
-      auto tO = [&](int t) { return tmem + (t ? L::kTmO1 : L::kTmO0); };
+      const uint32_t tS = tmem + (t ? L::kTmS1 : L::kTmS0), tO = tmem + (t ? L::kTmO1 : L::kTmO0);
       constexpr bool kTwo = L::kChunks == 2;
-      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t dK = kTwo ? smem_desc_sw32(sK, 2048) : smem_desc_sw128(sK, 16, 1024);
-      constexpr uint64_t kKStep = kTwo ? 16 : 2;
+      constexpr uint64_t kTileStep = L::kTileBytes >> 4;
+      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024) + t * kTileStep;
+      const uint64_t dK = smem_desc_sw128(sK, 16, L::kChunks * 1024);   // 8-row groups hold every chunk
       const int ps = a.page_size;
       const uint64_t dV = kTwo ? smem_desc_sw128(sV, static_cast<uint32_t>(ps) * 128u, ps >= 16 ? 1024u : 2048u)
                                : smem_desc_sw128(sV, L::kChunkBytes, 1024);
-      constexpr uint64_t kTileStep = L::kTileBytes >> 4;
       // page-major V: 16-key step kk starts at byte 2048 (kk + (kk & vmask))
       const int vmask = ~(max(ps / 16, 1) - 1);
-
-      auto issue_qk = [&](int t, int s) {   // S_t = Q_t K^T
-        uint64_t a0 = dQ + static_cast<uint64_t>(t) * kTileStep, b0 = dK + static_cast<uint64_t>(s) * kTileStep;
-        if (leader) {
-#pragma unroll 1
-          for (int c = 0; c < L::kChunks; ++c) {
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4)
-              mma_ss(tS(t), a0 + 2 * k4, b0 + kKStep * k4, idesc_qk, (c | k4) != 0 ? 1u : 0u);
-            a0 += L::kChunkBytes >> 4;
-            b0 += 4 * kKStep;
-          }
-        }
-        __syncwarp();
-      };
-      auto issue_pv_half = [&](int t, int s, int half, bool acc) {   // O_t += P_t V over 64 keys
-        const uint64_t b0 = dV + static_cast<uint64_t>(s) * kTileStep;
-        if (leader) {
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const int kk = half * 4 + k4;
-            const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
-            mma_ts(tO(t), tS(t) + kk * 8, b0 + static_cast<uint64_t>(off >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
-          }
-        }
-        __syncwarp();
-      };
-
       bool ok = true;
-      uint32_t g = 0;              // key tiles consumed
-      uint32_t steps_t[2] = {0, 0};   // S/P/O barrier phases of each row tile
-      int used[2] = {0, 0};        // segments whose O each row tile held
-      int qi = 0;
-      while (walk.more() && ok) {
-        const Segment sg = walk.next(a);
-        const int nt = sg.rows > kTile ? 2 : 1;
-        if (!(ok = mbar_wait_warp(BAR_Q, static_cast<uint32_t>(qi) & 1u, a.status, abort_flag))) break;
-        const int s0 = static_cast<int>(g % L::kStages);
-        if (!(ok = mbar_wait_warp(BAR_KF(s0), (g / L::kStages) & 1u, a.status, abort_flag))) break;
-        tc_fence_after();
-        for (int t = 0; t < nt; ++t) {
-          issue_qk(t, s0);
-          commit(BAR_SF(t));
-        }
-        commit(BAR_KE(s0));
-        if (sg.tiles == 1) commit(BAR_QE);
-        for (int j = 0; j < sg.tiles && ok; ++j) {
-          const uint32_t gj = g + static_cast<uint32_t>(j);
-          const int s = static_cast<int>(gj % L::kStages), s1 = static_cast<int>((gj + 1) % L::kStages);
-          if (!(ok = mbar_wait_warp(BAR_VF(s), (gj / L::kStages) & 1u, a.status, abort_flag))) break;
-          for (int t = 0; t < nt; ++t) {
-            const uint32_t c = steps_t[t];
-            // the first P.V of a segment overwrites O_t: the last segment's epilogue must have read it
-            if (j == 0 && used[t] > 0 &&
-                !(ok = mbar_wait_warp(BAR_OF(t), static_cast<uint32_t>(used[t] - 1) & 1u, a.status, abort_flag)))
-              break;
-            if (!(ok = mbar_wait_warp(BAR_PH(t), c & 1u, a.status, abort_flag))) break;
+      uint32_t steps_t = 0, used = 0;   // steps and segments of this row tile: S/P and Q/O barrier phases
+      for (uint32_t n = 0; ok; ++n) {
+        const uint32_t e = n % kSegments;
+        if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, a.status, abort_flag))) break;
+        // broadcasts tell the compiler that the values are the same in all lanes: the
+        // descriptors made of them stay in uniform registers
+        const uint32_t g0 = __shfl_sync(0xffffffffu, ring[e].g0, 0);
+        const int tiles = __shfl_sync(0xffffffffu, ring[e].tiles, 0);
+        const int wide = __shfl_sync(0xffffffffu, ring[e].wide, 0);
+        const int tile_first = __shfl_sync(0xffffffffu, ring[e].tile_first, 0);
+        const int own = __shfl_sync(0xffffffffu, ring[e].slot, 0) < 0, qslot = __shfl_sync(0xffffffffu, ring[e].qslot, 0);
+        if (leader) mbar_arrive(BAR_GE(e));
+        __syncwarp();
+        if (tiles == 0) break;
+        const int stride = wide ? 1 : 2, first = wide ? 0 : (t ^ tile_first) & 1;
+        if (first >= tiles) continue;
+        if (!(ok = wait_all(BAR_QF(t, used), (used / kQLoads) & 1u, a.status, abort_flag))) break;
+        if (own) {
+          // Few query rows: the products are taken with keys (S^T = K Q^T) and columns of
+          // d (O^T = V^T P^T) on the tensor memory's lanes and the queries on its columns.
+          // Every softmax thread then has one key and a handful of weights, and
+          // the products are an eighth as wide.  P^T comes from shared memory.
+          const uint64_t dQ1 = dQ + static_cast<uint64_t>(qslot * 64);
+          const uint64_t dP = smem_desc_sw128(sQ + t * L::kTileBytes + kOwnP, 16, 1024);
+          // with d = 64 rows 64..127 of V^T repeat others and are not read back
+          const uint64_t dVt = kTwo ? dV : smem_desc_sw128(sV, 1024, 1024);
+          constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kOwnCols, false);
+          constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, kOwnCols, false) | (1u << 15);   // A is d-major
+          for (int j = first; j < tiles; j += stride, ++steps_t) {
+            const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
+            if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, a.status, abort_flag))) break;
             tc_fence_after();
-            issue_pv_half(t, s, 0, j > 0);
-            if (!(ok = mbar_wait_warp(BAR_PR(t), c & 1u, a.status, abort_flag))) break;
-            tc_fence_after();
-            issue_pv_half(t, s, 1, true);
-            commit(BAR_OD(t));
-            if (j + 1 < sg.tiles) {
-              if (!(ok = mbar_wait_warp(BAR_KF(s1), ((gj + 1) / L::kStages) & 1u, a.status, abort_flag))) break;
-              issue_qk(t, s1);
-              commit(BAR_SF(t));
+            if (leader) {
+              uint64_t a0 = dK + ks * kTileStep, b0 = dQ1;
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                mma_ss(tS, a0, b0, idesc_s, k != 0 ? 1u : 0u);
+                a0 += (k & 3) == 3 ? (1024 >> 4) - 6 : 2;
+                b0 += (k & 3) == 3 ? (L::kChunkBytes >> 4) - 6 : 2;
+              }
+              mma_commit(BAR_SF(t));
+              mma_commit(BAR_KE(ks));
+              mbar_arrive(BAR_KE(ks));
             }
-            steps_t[t] = c + 1;
+            __syncwarp();
+            if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, a.status, abort_flag))) break;
+            if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, a.status, abort_flag))) break;
+            if (!(ok = wait_all(BAR_PR(t), steps_t & 1u, a.status, abort_flag))) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t a0 = dVt + vs * kTileStep;
+#pragma unroll 1
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
+                mma_ss(tO, a0 + static_cast<uint64_t>(off >> 4), dP + (kk >> 2) * (kOwnCols * 128 >> 4) + (kk & 3) * 2,
+                       idesc_o, (j > first || kk > 0) ? 1u : 0u);
+              }
+              if (j + stride >= tiles) mma_commit(BAR_OD(t));
+              mma_commit(BAR_VE(vs));
+              mbar_arrive(BAR_VE(vs));
+            }
+            __syncwarp();
+          }
+          ++used;
+          continue;
+        }
+        for (int j = first; j < tiles; j += stride, ++steps_t) {
+          const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
+          // S_t = Q_t K^T, 16 columns of d a step.  (The issue loops are rolled: a turn
+          // takes about the 64 cycles of its MMA, and the code stays small.)
+          if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, a.status, abort_flag))) break;
+          tc_fence_after();
+          if (leader) {
+            uint64_t a0 = dQ, b0 = dK + ks * kTileStep;
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              mma_ss(tS, a0, b0, idesc_qk, k != 0 ? 1u : 0u);
+              a0 += (k & 3) == 3 ? (L::kChunkBytes >> 4) - 6 : 2;   // within a 128-byte chunk, then the next one
+              b0 += (k & 3) == 3 ? (1024 >> 4) - 6 : 2;
+            }
+            mma_commit(BAR_SF(t));
+            mma_commit(BAR_KE(ks));   // K's release also frees the query tile after a segment's last step
+            if (!wide) mbar_arrive(BAR_KE(ks));
+          }
+          __syncwarp();
+          // O_t += P_t V, 64 keys as soon as their weights are written.  The first of a
+          // segment overwrites O_t: the epilogue before must have read it.
+          if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, a.status, abort_flag))) break;
+          if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, a.status, abort_flag))) break;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {   // BAR_PH(t), then BAR_PR(t)
+            if (!(ok = wait_all(BAR_PH(t) + 16u * half, steps_t & 1u, a.status, abort_flag))) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t b0 = dV + vs * kTileStep;
+#pragma unroll 1
+              for (int kk = half * 4; kk < half * 4 + 4; ++kk) {
+                const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
+                mma_ts(tO, tS + kk * 8, b0 + static_cast<uint64_t>(off >> 4), idesc_pv, (j > first || kk > 0) ? 1u : 0u);
+              }
+            }
+            __syncwarp();
           }
           if (!ok) break;
-          if (j + 2 == sg.tiles) commit(BAR_QE);   // the segment's last Q.K^T has been issued
-          commit(BAR_VE(s));
-          if (j + 1 < sg.tiles) commit(BAR_KE(s1));
+          if (leader) {
+            if (j + stride >= tiles) mma_commit(BAR_OD(t));   // the segment's O is complete
+            mma_commit(BAR_VE(vs));
+            if (!wide) mbar_arrive(BAR_VE(vs));
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        for (int t = 0; t < nt; ++t) ++used[t];
-        g += static_cast<uint32_t>(sg.tiles);
-        ++qi;
+        ++used;
       }
       // no commit may still be pending when the CTA exits
-      commit(BAR_FIN);
+      if (leader) mma_commit(BAR_FIN);
+      __syncwarp();
       mbar_wait_warp(BAR_FIN, 0, nullptr, nullptr);
     }
   } else {
-    setmaxnreg_inc<kRegsSoftmax>();
     // ======================= softmax warpgroups (one thread per query row) =======================
     const int t = (warp - kSoftmaxWarp0) / 4;
-    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const int quarter = warp & 3, lane_row = quarter * 32 + lane;   // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + (t == 0 ? L::kTmS0 : L::kTmS1) + lane_off;
     const uint32_t tO = tmem + (t == 0 ? L::kTmO0 : L::kTmO1) + lane_off;
     const float c2 = a.scale_log2;
     bool ok = true;
-    uint32_t steps_t = 0, g = 0;
-    while (walk.more() && ok) {
-      const Segment sg = walk.next(a);
-      if (t * kTile >= sg.rows) {   // this row tile has no rows
-        g += static_cast<uint32_t>(sg.tiles);
+    uint32_t steps_t = 0, held = 0, exchanges = 0;   // S/P and O barrier phases of this row tile
+    for (uint32_t seg = 0; ok; ++seg) {
+      const uint32_t e = seg % kSegments;
+      ok = wait_all(BAR_GF(e), (seg / kSegments) & 1u, a.status, abort_flag);
+      if (!ok) break;
+      const Segment sg = ring[e];
+      mbar_arrive(BAR_GE(e));
+      if (sg.tiles == 0) break;
+      // this row tile's steps j, j + stride, ...; `half`: which of the unit's two partials they make
+      const int stride = sg.wide ? 1 : 2, half = sg.wide ? t : (t ^ sg.tile_first) & 1;
+      const bool own = sg.slot < 0;
+      const int rows = sg.wide ? min(kTile, sg.rows - t * kTile) : sg.rows;   // of this tile
+      const int row = lane_row;
+      const bool live = row < rows, warp_live = quarter * 32 < rows;
+      int j = sg.wide ? 0 : half;
+      if (j >= sg.tiles) continue;
+      // V rows that are no key get weight 0, and whatever is there must not turn
+      // that into NaN: they are zeroed before the products read them (wide steps: by
+      // both row tiles' warps, each before its own product).
+      auto zero_values = [&](int j, int lo, int lim) {
+        const uint32_t gj = sg.g0 + static_cast<uint32_t>(j), sv = gj % VS;
+        if (!wait_all(BAR_VF(sv), (gj / VS) & 1u, a.status, abort_flag)) return false;
+        if (lane_row >= lim || lane_row < lo) {
+          const int pr = lane_row % a.page_size;
+          uint8_t* base = smem + L::kV + sv * L::kTileBytes + (lane_row - pr) * D * 2 + pr * 128;
+#pragma unroll 1
+          for (int c = 0; c < L::kChunks; ++c)
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              reinterpret_cast<uint4*>(base + c * a.page_size * 128)[z] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return true;
+      };
+      if (own) {
+        // ---- own keys: this thread has key `lane_row` of the tile and one score per query row
+        constexpr int kG = 8;
+        const int G = a.G;
+        float m[kG], l[kG];
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+          m[i] = -INFINITY;
+          l[i] = 0.f;
+        }
+        // eight values of each of the row tile's four warps, joined through shared memory
+        float* red = reinterpret_cast<float*>(smem + L::kRed) + t * 2 * 4 * kG;
+        auto exchange = [&](float (&v)[kG], auto join) {
+          float* buf = red + (exchanges & 1u) * 4 * kG;   // two in turn: one barrier an exchange
+          if (lane == 0) {
+            reinterpret_cast<float4*>(buf + quarter * kG)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(buf + quarter * kG)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            mbar_arrive(BAR_X(t));
+          }
+          if (!wait_all(BAR_X(t), exchanges++ & 1u, a.status, abort_flag)) return false;
+#pragma unroll
+          for (int i = 0; i < kG; i += 4) {
+            float4 x = *reinterpret_cast<const float4*>(buf + i);
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+              const float4 y = *reinterpret_cast<const float4*>(buf + w * kG + i);
+              x = make_float4(join(x.x, y.x), join(x.y, y.y), join(x.z, y.z), join(x.w, y.w));
+            }
+            v[i] = x.x;
+            v[i + 1] = x.y;
+            v[i + 2] = x.z;
+            v[i + 3] = x.w;
+          }
+          return true;
+        };
+        uint8_t* prow = smem + L::kQ + t * L::kTileBytes + kOwnP + (lane_row >> 6) * (kOwnCols * 128);
+        for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t) {
+          ok = wait_all(BAR_SF(t), steps_t & 1u, a.status, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
+          const bool is_key = lane_row >= lo && lane_row < lim;
+          if ((lim < kTile || lo > 0) && !(ok = zero_values(j, lo, lim))) break;
+          uint32_t sr[kG];
+          tmem_ld8(tS, sr);
+          tmem_wait_ld();
+          float s[kG], mx[kG];
+#pragma unroll
+          for (int i = 0; i < kG; ++i) {
+            s[i] = is_key ? __uint_as_float(sr[i]) : -INFINITY;
+            mx[i] = warp_max(s[i]);
+          }
+          if (!(ok = exchange(mx, [](float x, float y) { return fmaxf(x, y); }))) break;
+          float alpha[kG];
+          bool rescale = false;
+#pragma unroll
+          for (int i = 0; i < kG; ++i) {
+            const float m_new = fmaxf(m[i], mx[i]);
+            const bool upd = (m[i] == -INFINITY) || ((m_new - m[i]) * c2 > kRescaleLog2);
+            alpha[i] = (upd && m[i] != -INFINITY) ? ex2((m[i] - m_new) * c2) : 1.f;
+            if (upd) m[i] = m_new;
+            rescale = rescale || (i < G && alpha[i] != 1.f);
+          }
+          if (!first && rescale) {   // all 128 threads alike
+            uint32_t orr[kG];
+            tmem_ld8(tO, orr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < kG; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha[i]);
+            tmem_st8(tO, orr);
+            tmem_wait_st();
+          }
+          // weights into P^T [query][key], 128-byte rows of 64 keys, 16-byte pieces swizzled by the row
+#pragma unroll
+          for (int i = 0; i < kG; ++i) {
+            const float negm = (m[i] == -INFINITY) ? 0.f : -m[i] * c2;
+            const float p = ex2(fmaf(s[i], c2, negm));
+            l[i] = fmaf(l[i], alpha[i], p);
+            if (i < G)
+              *reinterpret_cast<__nv_bfloat16*>(prow + i * 128 + ((((lane_row & 63) >> 3) ^ i) << 4) + (lane_row & 7) * 2) =
+                  __float2bfloat16(p);
+          }
+          fence_proxy_async_smem();   // P (and zeroed V) before the products read them
+          tc_fence_before();
+          mbar_arrive(BAR_PR(t));
+        }
+        if (!ok) break;
+        // ---- the partial: this thread has column `lane_row` of d
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+#pragma unroll
+          for (int x = 16; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        ok = exchange(l, [](float x, float y) { return x + y; }) && wait_all(BAR_OD(t), held & 1u, a.status, abort_flag);
+        tc_fence_after();
+        if (!ok) break;
+        ++held;
+        uint32_t orr[kG];
+        tmem_ld8(tO, orr);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(BAR_OF(t));
+        const size_t at = (static_cast<size_t>(~sg.slot) * 2 + half) * G;
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+          if (i < G) {
+            const float inv = l[i] > 0.f ? __fdividef(1.f, l[i]) : 0.f;
+            if (lane_row < D) a.own_o[(at + i) * D + lane_row] = __uint_as_float(orr[i]) * inv;
+            if (lane_row == i)
+              a.own_lse[at + i] = l[i] > 0.f ? fmaf(m[i], a.scale, __log2f(l[i]) * 0.69314718055994531f) : -INFINITY;
+          }
         continue;
       }
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < sg.tiles; ++j, ++g) {
-        ok = __all_sync(0xffffffffu, mbar_wait(BAR_SF(t), (steps_t + j) & 1u, a.status, abort_flag));
+      for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t) {
+        ok = wait_all(BAR_SF(t), steps_t & 1u, a.status, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
-        tmem_wait_ld();
-        float* s = reinterpret_cast<float*>(&sr[0][0]);
-        // keys of this tile: [0, lim); the rest of its shared memory holds no key
-        const int lim = min(kTile, sg.len - (sg.tile0 + j) * kTile);
-        const bool need_mask = lim < kTile;
+        // keys of this tile: columns [lo, lim); the rest of its shared memory holds none that count
+        const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
+        const bool need_mask = lim < kTile || lo > 0;
         if (need_mask) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : -INFINITY;
-          // V rows past the keys get weight 0, and whatever is there must not
-          // turn that into NaN: the first row tile's warps zero them (its P.V is
-          // issued first).
-          if (t == 0) {
-            const int sv = static_cast<int>(g % L::kStages);
-            ok = __all_sync(0xffffffffu, mbar_wait(BAR_VF(sv), (g / L::kStages) & 1u, a.status, abort_flag));
-            if (!ok) break;
-            if (row >= lim) {
-              const int pr = row % a.page_size;
-              uint8_t* base = smem + L::kV + sv * L::kTileBytes + (row - pr) * D * 2 + pr * 128;
-#pragma unroll
-              for (int c = 0; c < L::kChunks; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  reinterpret_cast<uint4*>(base + c * a.page_size * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();   // before the products read them
-          }
+          if (!(ok = zero_values(j, lo, lim))) break;
+          fence_proxy_async_smem();
         }
-        // 64 columns: weights 2^((s - m) c2), packed to bf16; the sum of the
-        // unrounded values.  Masked columns are exactly 0.
-        auto exp_half = [&](auto masked, int h, float negm, uint32_t (&pk)[32]) -> float {
-          constexpr bool kMasked = decltype(masked)::value;
-          const float2 c2v = make_float2(c2, c2), negv = make_float2(negm, negm);
-          float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
+        if (!warp_live) {   // no row of this warp counts: its P may hold anything
+          mbar_arrive(BAR_PH(t));
+          mbar_arrive(BAR_PR(t));
+          continue;
+        }
+        // Two passes over the scores in TMEM, 32 columns at a time: the row max,
+        // then the weights.  Loading them twice costs less than holding all 128
+        // in registers with the code unrolled over them: that code did not fit the
+        // instruction cache beside the other roles (see the top of the file).
+        auto load = [&](int c0, uint32_t (&r)[32]) {
+          tmem_ld32(tS + c0, r);
+          tmem_wait_ld();
+          if (need_mask) {
+            // bit c: column c0 + c is a key
+            const int a0 = max(lo - c0, 0), b0 = min(max(lim - c0, 0), 32);
+            const uint32_t keys = b0 > a0 ? (0xffffffffu >> (32 - b0)) & (0xffffffffu << a0) : 0u;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int c = h * 64 + 2 * i;
-            const float2 x = ffma2(make_float2(s[c], s[c + 1]), c2v, negv);
-            float2 pp = make_float2(ex2(x.x), ex2(x.y));
-            if constexpr (kMasked) {
-              pp.x = c < lim ? pp.x : 0.f;
-              pp.y = c + 1 < lim ? pp.y : 0.f;
-            }
-            if (i & 1) sb = fadd2(sb, pp);
-            else sa = fadd2(sa, pp);
-            pk[i] = pack_bf16x2(pp.x, pp.y);
+            for (int c = 0; c < 32; ++c)
+              if (!(keys >> c & 1u)) r[c] = __float_as_uint(-INFINITY);
           }
-          return (sa.x + sb.x) + (sa.y + sb.y);
         };
-        auto exp_half_any = [&](int h, float negm, uint32_t (&pk)[32]) -> float {
-          return need_mask ? exp_half(std::true_type{}, h, negm, pk) : exp_half(std::false_type{}, h, negm, pk);
-        };
-        float mx;
-        {
-          float r0 = -INFINITY, r1 = -INFINITY, r2 = -INFINITY, r3 = -INFINITY;
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTile; c0 += 32) {
+          uint32_t sr[32];
+          load(c0, sr);
+          const float* s = reinterpret_cast<const float*>(sr);
+          float r0 = -INFINITY, r1 = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
+          for (int c = 0; c < 32; c += 4) {
             r0 = fmax3(r0, s[c + 0], s[c + 1]);
             r1 = fmax3(r1, s[c + 2], s[c + 3]);
-            r2 = fmax3(r2, s[c + 4], s[c + 5]);
-            r3 = fmax3(r3, s[c + 6], s[c + 7]);
           }
-          mx = fmaxf(fmax3(r0, r1, r2), r3);
+          mx = fmax3(mx, r0, r1);
         }
         const float m_new = fmaxf(m, mx);
         const bool upd = (m == -INFINITY) || ((m_new - m) * c2 > kRescaleLog2);
@@ -597,64 +956,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = (upd && m != -INFINITY) ? ex2((m - m_use) * c2) : (m == -INFINITY ? 0.f : 1.f);
         const float negm = (m_use == -INFINITY) ? 0.f : -m_use * c2;
         m = m_use;
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // rows that do not count hold anything: they ask for no rescale
+        if (!first && __any_sync(0xffffffffu, live && alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t orr[32];
             tmem_ld32(tO + c * 32, orr);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+            for (int z = 0; z < 32; ++z) orr[z] = __float_as_uint(__uint_as_float(orr[z]) * alpha);
             tmem_st32(tO + c * 32, orr);
           }
         }
-        float psum;
-        {
-          uint32_t pk[32];
-          psum = exp_half_any(0, negm, pk);
-          tmem_st32(tS, pk);
+        l *= alpha;
+        // Weights 2^((s - m) c2), packed to bf16 for the tensor product (the rounding
+        // of the prefill kernels; the sum is of the unrounded values).  c2 > 0 (see
+        // the host side), so masked columns are exactly 0.  The weights take the columns
+        // of scores already read.
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTile; c0 += 32) {
+          uint32_t sr[32], pk[16];
+          load(c0, sr);
+          const float* s = reinterpret_cast<const float*>(sr);
+          const float2 c2v = make_float2(c2, c2), negv = make_float2(negm, negm);
+          float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), c2v, negv);
+            const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+            if (i & 1) sb = fadd2(sb, pp);
+            else sa = fadd2(sa, pp);
+            pk[i] = pack_bf16x2(pp.x, pp.y);
+          }
+          l += (sa.x + sb.x) + (sa.y + sb.y);
+          tmem_st16(tS + (c0 >> 1), pk);
+          if (c0 & 32) {   // a half is written: the MMA warp starts on the first meanwhile
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(c0 < 64 ? BAR_PH(t) : BAR_PR(t));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(BAR_PH(t));
-        {
-          uint32_t pk[32];
-          psum += exp_half_any(1, negm, pk);
-          tmem_st32(tS + 32, pk);
-        }
-        l = alpha * l + psum;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(BAR_PR(t));
       }
       if (!ok) break;
-      // ---- the segment's partial: O / l and m scale + ln l, in fp32
-      ok = __all_sync(0xffffffffu, mbar_wait(BAR_OD(t), (steps_t + sg.tiles - 1) & 1u, a.status, abort_flag));
+      // ---- the partial: O / l and m scale + ln l, in fp32
+      ok = wait_all(BAR_OD(t), held & 1u, a.status, abort_flag);
       tc_fence_after();
       if (!ok) break;
-      steps_t += static_cast<uint32_t>(sg.tiles);
-      const int urow = t * kTile + row;
-      const bool store = urow < sg.rows;
-      const float inv = (l > 0.f) ? 1.f / l : 0.f;
-      float4* dst = reinterpret_cast<float4*>(a.pre_o) + static_cast<size_t>(sg.slot) * (D / 4) * kUnitRows + urow;
+      ++held;
+      if (warp_live) {
+        const size_t slot = static_cast<size_t>(sg.slot);
+        const float inv = (l > 0.f) ? 1.f / l : 0.f;
+        // [slot][4 columns][256 rows]: a warp's rows side by side
+        float4* dst = reinterpret_cast<float4*>(a.pre_o) + slot * (D / 4) * kUnitRows + half * kTile + row;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t orr[32];
-        tmem_ld32(tO + c * 32, orr);
-        tmem_wait_ld();
-        if (store) {
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t orr[32];
+          tmem_ld32(tO + c * 32, orr);
+          tmem_wait_ld();
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[(c * 8 + e) * kUnitRows] =
-                make_float4(__uint_as_float(orr[4 * e]) * inv, __uint_as_float(orr[4 * e + 1]) * inv,
-                            __uint_as_float(orr[4 * e + 2]) * inv, __uint_as_float(orr[4 * e + 3]) * inv);
+            for (int z = 0; z < 8; ++z)
+              dst[(c * 8 + z) * kUnitRows] =
+                  make_float4(__uint_as_float(orr[4 * z]) * inv, __uint_as_float(orr[4 * z + 1]) * inv,
+                              __uint_as_float(orr[4 * z + 2]) * inv, __uint_as_float(orr[4 * z + 3]) * inv);
+          }
+        }
+        if (live) {
+          a.pre_lse[slot * kUnitRows + half * kTile + row] =
+              (l > 0.f) ? fmaf(m, a.scale, __log2f(l) * 0.69314718055994531f) : -INFINITY;
         }
       }
       tc_fence_before();
       mbar_arrive(BAR_OF(t));
-      if (store)
-        a.pre_lse[static_cast<size_t>(sg.slot) * kUnitRows + urow] =
-            (l > 0.f) ? fmaf(m, a.scale, __log2f(l) * 0.69314718055994531f) : -INFINITY;
     }
   }
 
@@ -675,6 +1048,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kCombineThreads = 256;
 
+// The CTAs [c0, c0 + n) that hold partials of a unit at place x0 on the line.
+__device__ __forceinline__ void unit_ctas(long long x0, int tiles, int shift, long long per, long long& c0, int& n) {
+  c0 = x0 / per;
+  n = static_cast<int>((x0 + (static_cast<long long>(tiles - 1) << shift)) / per - c0) + 1;
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const SharedArgs a, __nv_bfloat16* o,
                                                                        float* lse) {
@@ -684,43 +1063,12 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
   __shared__ float4 s_o[kCombineThreads];
   const int hkv = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
   const int p0 = tid / kPer, c4 = (tid % kPer) / G, gq = tid % G;
-  grid_wait();   // both kernels that write partials are complete
-  const int cap = a.max_pages * a.page_size;
-  const int start = a.own_start[seq], of = a.group_of[seq];
-  int len = min(max(__ldg(a.seq_lens + seq), 0), cap);
-  len = min(len, start + a.max_own);
-  const int split_tokens = a.own_split_pages * a.page_size;
-  const int base = start / a.page_size * a.page_size;
-  const int n_own = len > start ? (len - base + split_tokens - 1) / split_tokens : 0;
-  int n_pre = 0, urow = 0;
-  long long slot0 = 0;
-  if (of >= 0) {
-    const Group r = a.groups[of];
-    const int tiles = prefix_tiles(r.len), blocks = row_blocks(r.n, G), rr = (seq - r.first) * G + gq;
-    const long long unit = static_cast<long long>(hkv) * blocks + rr / kUnitRows;
-    const long long x0 = r.step0 + unit * tiles, per = a.header->per_cta;
-    const long long c0 = x0 / per, c1 = (x0 + tiles - 1) / per;
-    n_pre = static_cast<int>(c1 - c0 + 1);
-    slot0 = c0 + r.unit0 + unit;
-    urow = rr % kUnitRows;
-  }
-  const int hq = hkv * G + gq;
-  const size_t own0 = (static_cast<size_t>(seq) * a.Hq + hq) * a.own_splits;
-
+  grid_wait();   // the partials are complete
+  const long long per = a.header->per_cta;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = p0; i < n_pre + n_own; i += NP) {
-    float w;
-    float4 v;
-    if (i < n_pre) {
-      w = a.pre_lse[(slot0 + i) * kUnitRows + urow];
-      v = reinterpret_cast<const float4*>(a.pre_o)[((slot0 + i) * (D / 4) + c4) * kUnitRows + urow];
-    } else {
-      w = a.own_lse[own0 + i - n_pre];
-      v = reinterpret_cast<const float4*>(a.own_o + (own0 + i - n_pre) * D)[c4];
-    }
-    if (w == -INFINITY) continue;
+  auto join = [&](float w, const float4& v) {
+    if (w == -INFINITY) return;
     const float mn = fmaxf(m, w), s0 = __expf(m - mn), s1 = __expf(w - mn);
     l = fmaf(l, s0, s1);
     acc.x = fmaf(acc.x, s0, s1 * v.x);
@@ -728,6 +1076,54 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
     acc.z = fmaf(acc.z, s0, s1 * v.z);
     acc.w = fmaf(acc.w, s0, s1 * v.w);
     m = mn;
+  };
+  // A narrow segment of two or more steps made two partials, one of a single step one.
+  const int of = a.group_of[seq];
+  if (of >= 0) {
+    const Item it = a.items[of];
+    const int tiles = item_tiles(it), blocks = item_blocks(it, G), shift = item_shift(it, G);
+    const int r = (seq - it.first) * G + gq, block = r / kUnitRows, unit = hkv * blocks + block;
+    const int urow = r % kUnitRows;
+    const bool wide = min(kUnitRows, it.n * G - block * kUnitRows) > kTile;
+    const long long x0 = it.x0 + ((static_cast<long long>(unit) * tiles) << shift);
+    long long c0;
+    int n;
+    unit_ctas(x0, tiles, shift, per, c0, n);
+    const size_t slot0 = static_cast<size_t>(c0) + it.unit0 + unit;
+#pragma unroll 4
+    for (int i = p0; i < (wide ? n : 2 * n); i += NP) {
+      const int k = wide ? i : i >> 1, h = wide ? 0 : i & 1;
+      if (h) {
+        int j0, j1;
+        unit_share(x0, tiles, shift, per, static_cast<int>(c0) + k, j0, j1);
+        if (j1 - j0 < 2) continue;
+      }
+      const size_t at = (slot0 + k) * kUnitRows + h * kTile + urow;
+      join(a.pre_lse[at], reinterpret_cast<const float4*>(a.pre_o)[(slot0 + k) * (D / 4) * kUnitRows +
+                                                                  static_cast<size_t>(c4) * kUnitRows + h * kTile + urow]);
+    }
+  }
+  {
+    const Item it = a.items[a.num_groups + seq];
+    const int tiles = item_tiles(it);
+    if (tiles > 0) {
+      const long long x0 = it.x0 + static_cast<long long>(hkv) * tiles;
+      long long c0;
+      int n;
+      unit_ctas(x0, tiles, 0, per, c0, n);
+      const size_t slot0 = static_cast<size_t>(c0) + it.unit0 + hkv;
+#pragma unroll 4
+      for (int i = p0; i < 2 * n; i += NP) {
+        const int k = i >> 1, h = i & 1;
+        if (h) {
+          int j0, j1;
+          unit_share(x0, tiles, 0, per, static_cast<int>(c0) + k, j0, j1);
+          if (j1 - j0 < 2) continue;
+        }
+        const size_t at = ((slot0 + k) * 2 + h) * G + gq;
+        join(a.own_lse[at], reinterpret_cast<const float4*>(a.own_o)[at * (D / 4) + c4]);
+      }
+    }
   }
   s_m[tid] = m;
   s_l[tid] = l;
@@ -750,7 +1146,7 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
     out.w = fmaf(w, v.w, out.w);
   }
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  const size_t orow = static_cast<size_t>(seq) * a.Hq + hq;
+  const size_t orow = static_cast<size_t>(seq) * a.Hq + hkv * G + gq;
   uint2 w2;
   w2.x = pack_bf16x2(out.x * inv, out.y * inv);
   w2.y = pack_bf16x2(out.z * inv, out.w * inv);
@@ -763,90 +1159,94 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
 // ---------------------------------------------------------------------------
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// pdl: programmatic dependent of the kernel before
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, bool pdl, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D>
-ta_status launch_prefix(const void* q, const void* k_cache, const void* v_cache, const SharedArgs& a,
+ta_status launch_attend(const void* q, const void* k_cache, const void* v_cache, const SharedArgs& a,
                         cudaStream_t stream) {
-  using L = PrefixLayout<D>;
-  CUtensorMap tq, tk, tv;
+  using L = AttendLayout<D>;
+  CUtensorMap tq, tq1, tk, tv;
   ta_status st;
-  {  // queries [S, Hq, d] as {64, Hq, S, d / 64}: a box of G heads of 128 / G sequences is one tile of 128 rows
-    const uint64_t dims[4] = {64, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.num_seqs), D / 64};
-    const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.Hq) * D * 2, 128};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(kTile / a.G), D / 64};
-    if ((st = encode_bf16_tiled(&tq, q, 4, dims, strides, box)) != TA_OK) return st;
+  // queries [S, Hq, d] as {64, Hq, S, d / 64}: a box of G heads of 128 / G sequences is one tile of 128 rows, a box
+  // of G heads of one sequence one chunk of the rows that meet its own keys
+  const uint64_t dims[4] = {64, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.num_seqs), D / 64};
+  const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.Hq) * D * 2, 128};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(kTile / a.G), D / 64};
+  const uint32_t box1[4] = {64, static_cast<uint32_t>(a.G), 1, 1};
+  if ((st = encode_bf16_tiled(&tq, q, 4, dims, strides, box)) != TA_OK) return st;
+  if ((st = encode_bf16_tiled(&tq1, q, 4, dims, strides, box1)) != TA_OK) return st;
+  {  // one page of one KV head a copy
+    const uint64_t row = static_cast<uint64_t>(D) * 2, ps = static_cast<uint64_t>(a.page_size);
+    const uint64_t heads = static_cast<uint64_t>(a.Hkv), pages = static_cast<uint64_t>(a.num_pages_total);
+    const uint32_t rows = static_cast<uint32_t>(a.page_size), chunks = D / 64;
+    // K as {64 columns, 8 rows, chunk, 8-row group, page and head}: lands [8-row group][chunk][8 rows][128 B], so all
+    // 128 keys of a tile are 8-row groups at one stride, whichever page they came from
+    const uint64_t dk[5] = {64, 8, chunks, ps / 8, pages * heads}, sk[4] = {row, 128, 8 * row, ps * row};
+    const uint32_t bk[5] = {64, 8, chunks, rows / 8, 1};
+    if ((st = encode_bf16_tiled(&tk, k_cache, 5, dk, sk, bk)) != TA_OK) return st;
+    // V as {64 columns, page rows, chunk, head, page}: lands [chunk][page rows][128 B]
+    const uint64_t dv[5] = {64, ps, chunks, heads, pages}, sv[4] = {row, 128, ps * row, heads * ps * row};
+    const uint32_t bv[5] = {64, rows, chunks, 1, 1};
+    if ((st = encode_bf16_tiled(&tv, v_cache, 5, dv, sv, bv)) != TA_OK) return st;
   }
-  if ((st = encode_pool_maps(&tk, &tv, k_cache, v_cache, D, a.page_size, a.Hkv, a.num_pages_total)) != TA_OK) return st;
   static int attr_done[64] = {0};
-  cudaError_t e = ensure_smem_limit(prefix_kernel<D>, L::kAlloc, attr_done);
+  cudaError_t e = ensure_smem_limit(shared_attend_kernel<D>, L::kAlloc, attr_done);
   if (e != cudaSuccess) return fail(TA_ERR_CUDA, "shared decode: shared-memory limit", e);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = L::kAlloc;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefix_kernel<D>, tq, tk, tv, a);
-  return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: prefix kernel launch", e);
-}
-
-template <int D, int G>
-cudaError_t launch_combine(const SharedArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.num_seqs));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_combine_kernel<D, G>, a, o, lse);
+  e = launch(shared_attend_kernel<D>, dim3(static_cast<unsigned>(a.n_ctas)), kThreads, L::kAlloc, true, stream, tq, tq1,
+             tk, tv, a);
+  return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: attend kernel launch", e);
 }
 
 template <int D>
-cudaError_t launch_combine_g(const SharedArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
+cudaError_t launch_combine(const SharedArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.num_seqs));
   switch (a.G) {
-    case 1: return launch_combine<D, 1>(a, o, lse, stream);
-    case 2: return launch_combine<D, 2>(a, o, lse, stream);
-    case 4: return launch_combine<D, 4>(a, o, lse, stream);
-    default: return launch_combine<D, 8>(a, o, lse, stream);
+    case 1: return launch(shared_combine_kernel<D, 1>, grid, kCombineThreads, 0, true, stream, a, o, lse);
+    case 2: return launch(shared_combine_kernel<D, 2>, grid, kCombineThreads, 0, true, stream, a, o, lse);
+    case 4: return launch(shared_combine_kernel<D, 4>, grid, kCombineThreads, 0, true, stream, a, o, lse);
+    default: return launch(shared_combine_kernel<D, 8>, grid, kCombineThreads, 0, true, stream, a, o, lse);
   }
 }
 
 }  // namespace
 
-bool make_shared_plan(int num_seqs, int num_groups, int Hq, int Hkv, int d, int max_own_len, int page_size,
-                      SharedPlan* p) {
-  if (num_seqs < 0 || num_groups < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || max_own_len < 0 || page_size <= 0) return false;
+bool make_shared_plan(int num_seqs, int num_groups, int Hq, int Hkv, int d, SharedPlan* p) {
+  if (num_seqs < 0 || num_groups < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || (d != 64 && d != 128)) return false;
   const int G = Hq / Hkv;
   if ((G != 1 && G != 2 && G != 4 && G != 8) || num_seqs > 65535 || Hkv > 65535 || num_groups > 65535) return false;
-  // own keys start inside a page at worst: one page more than their own
-  const int own_pages = max_own_len == 0 ? 0 : (max_own_len + page_size - 1) / page_size + 1;
-  if (!make_decode_plan(num_seqs, Hq, Hkv, d, own_pages > 0 ? own_pages : 1, page_size, &p->own)) return false;
-  if (own_pages == 0) p->own.max_splits = 0;
   p->n_ctas = current_sm_count();
-  // units: every group has at most one block of rows that is not full, per KV head
-  const long long units = num_groups == 0 ? 0 : static_cast<long long>(Hkv) * (num_groups + static_cast<long long>(num_seqs) * G / kUnitRows);
+  // prefix units: every group has at most one block of rows that is not full, per KV head
+  const long long units =
+      num_groups == 0 ? 0 : static_cast<long long>(Hkv) * (num_groups + static_cast<long long>(num_seqs) * G / kUnitRows);
   const long long slots = units == 0 ? 0 : units + p->n_ctas;
-  if (slots > INT32_MAX) return false;
+  const long long own_slots = static_cast<long long>(num_seqs) * Hkv + p->n_ctas;
+  if (slots > INT32_MAX || own_slots > INT32_MAX) return false;
   size_t at = 512;   // status word, plan header
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = up256(at + bytes);
     return here;
   };
-  p->groups = take((static_cast<size_t>(num_groups) + 1) * sizeof(Group));
-  p->own_start = take(static_cast<size_t>(num_seqs) * 4);
+  p->items = take((static_cast<size_t>(num_groups) + num_seqs + 1) * sizeof(Item));
   p->group_of = take(static_cast<size_t>(num_seqs) * 4);
   p->pre_o = take(static_cast<size_t>(slots) * kUnitRows * d * 4);
   p->pre_lse = take(static_cast<size_t>(slots) * kUnitRows * 4);
-  const size_t rows = static_cast<size_t>(num_seqs) * Hq * p->own.max_splits;
-  p->own_o = take(rows * d * 4);
-  p->own_lse = take(rows * 4);
+  p->own_o = take(static_cast<size_t>(own_slots) * 2 * G * d * 4);
+  p->own_lse = take(static_cast<size_t>(own_slots) * 2 * G * 4);
   p->bytes = at;
   return true;
 }
@@ -871,38 +1271,27 @@ ta_status launch_decode_shared(const void* q, const void* k_cache, const void* v
   a.max_pages = max_pages;
   a.num_pages_total = num_pages_total;
   a.n_ctas = plan.n_ctas;
-  a.own_splits = plan.own.max_splits;
-  a.own_split_pages = plan.own.split_pages;
   a.max_own = max_own_len;
   a.scale = scale;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // a scale of 0 (equal weights) becomes one so small that finite scores still weigh 1: masked scores are -inf, and
+  // 0 times that would be NaN
+  a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1e-30f);
   a.status = reinterpret_cast<unsigned*>(ws);
   a.header = reinterpret_cast<PlanHeader*>(ws + 256);
-  a.groups = reinterpret_cast<Group*>(ws + plan.groups);
-  a.own_start = reinterpret_cast<int32_t*>(ws + plan.own_start);
+  a.items = reinterpret_cast<Item*>(ws + plan.items);
   a.group_of = reinterpret_cast<int32_t*>(ws + plan.group_of);
   a.pre_o = reinterpret_cast<float*>(ws + plan.pre_o);
   a.pre_lse = reinterpret_cast<float*>(ws + plan.pre_lse);
   a.own_o = reinterpret_cast<float*>(ws + plan.own_o);
   a.own_lse = reinterpret_cast<float*>(ws + plan.own_lse);
 
-  shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch(shared_plan_kernel, dim3(1), kPlanThreads, 0, false, stream, a);
   if (e != cudaSuccess) return fail(TA_ERR_CUDA, "shared decode: plan kernel launch", e);
-  if (num_groups > 0) {
-    const ta_status st = d == 128 ? launch_prefix<128>(q, k_cache, v_cache, a, stream)
-                                  : launch_prefix<64>(q, k_cache, v_cache, a, stream);
-    if (st != TA_OK) return st;
-  }
-  if (plan.own.max_splits > 0) {
-    // without a prefix kernel in between it has to wait for the plan kernel: an ordinary launch
-    e = launch_decode_own(q, k_cache, v_cache, block_table, seq_lens, a.own_start, max_own_len, page_size, num_seqs,
-                          Hq, Hkv, d, max_pages, num_pages_total, scale, plan.own, a.own_o, a.own_lse, a.status,
-                          num_groups > 0, stream);
-    if (e != cudaSuccess) return fail(TA_ERR_CUDA, "shared decode: own-keys kernel launch", e);
-  }
+  const ta_status st = d == 128 ? launch_attend<128>(q, k_cache, v_cache, a, stream)
+                                : launch_attend<64>(q, k_cache, v_cache, a, stream);
+  if (st != TA_OK) return st;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(o);
-  e = d == 128 ? launch_combine_g<128>(a, out, lse, stream) : launch_combine_g<64>(a, out, lse, stream);
+  e = d == 128 ? launch_combine<128>(a, out, lse, stream) : launch_combine<64>(a, out, lse, stream);
   return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: combine kernel launch", e);
 }
 

@@ -831,7 +831,34 @@ static ta_status launch_paged_prefill_d(const void* q, const void* k_cache, cons
     const uint32_t box[4] = {64, 1, 128, D / 64};
     if ((st = encode_bf16_tiled(&tq, q, 4, dims, strides, box)) != TA_OK) return st;
   }
-  if ((st = encode_pool_maps(&tk, &tv, k_cache, v_cache, D, page_size, Hkv, num_pages_total)) != TA_OK) return st;
+  {  // pool [P, Hkv, page, d]: boxes of one page of one KV head
+    const uint64_t dims[4] = {D, static_cast<uint64_t>(page_size), static_cast<uint64_t>(Hkv),
+                              static_cast<uint64_t>(num_pages_total)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(page_size) * D * 2,
+                                 static_cast<uint64_t>(Hkv) * page_size * D * 2};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(page_size), 1, 1};
+    if (L::kChunks == 1) {
+      if ((st = encode_bf16_tiled(&tk, k_cache, 4, dims, strides, box)) != TA_OK) return st;
+      if ((st = encode_bf16_tiled(&tv, v_cache, 4, dims, strides, box)) != TA_OK) return st;
+    } else {
+      // K: [P, Hkv, page, 128] seen as 5-D {16 columns, 8 rows, 8 column groups, page / 8 row
+      // groups, P * Hkv (page, head) blocks}, box {16, 8, 8, page / 8, 1}, 32-byte swizzle: one
+      // copy lands a page as [row group][column group][8 rows][32 B]
+      const uint64_t dk[5] = {16, 8, 8, static_cast<uint64_t>(page_size / 8),
+                              static_cast<uint64_t>(num_pages_total) * Hkv};
+      const uint64_t sk[4] = {static_cast<uint64_t>(D) * 2, 32, 8ull * D * 2, static_cast<uint64_t>(page_size) * D * 2};
+      const uint32_t bk[5] = {16, 8, 8, static_cast<uint32_t>(page_size / 8), 1};
+      if ((st = encode_bf16_tiled_sw32(&tk, k_cache, 5, dk, sk, bk)) != TA_OK) return st;
+      // V: [P, Hkv, page, (2 chunks of 64)] seen as 5-D {64, page, chunk, Hkv, P}, so that one box
+      // {64, page, 2, 1, 1} lands a page as [chunk][page rows][128 B]
+      const uint64_t dv[5] = {64, static_cast<uint64_t>(page_size), 2, static_cast<uint64_t>(Hkv),
+                              static_cast<uint64_t>(num_pages_total)};
+      const uint64_t sv[4] = {static_cast<uint64_t>(D) * 2, 128, static_cast<uint64_t>(page_size) * D * 2,
+                              static_cast<uint64_t>(Hkv) * page_size * D * 2};
+      const uint32_t bv[5] = {64, static_cast<uint32_t>(page_size), 2, 1, 1};
+      if ((st = encode_bf16_tiled(&tv, v_cache, 5, dv, sv, bv)) != TA_OK) return st;
+    }
+  }
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_limit(prefill_fwd_kernel<D, true, false>, L::kAlloc, attr_done);
   if (e != cudaSuccess) return fail(TA_ERR_CUDA, "paged prefill: shared-memory limit", e);

@@ -34,12 +34,6 @@ ta_status encode_bf16_tiled(CUtensorMap* map, const void* base, int rank, const 
 ta_status encode_bf16_tiled_sw32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                                  const uint64_t* strides_bytes, const uint32_t* box);
 
-// Tensor maps over a page pool [num_pages, Hkv, page_size, d] whose box is one
-// page of one KV head (d = 64: 4-D {64, page, Hkv, P}; d = 128: 5-D, K in the
-// 32-byte swizzle, V as [chunk][page rows][128 B]; see the paged prefill).
-ta_status encode_pool_maps(CUtensorMap* k_map, CUtensorMap* v_map, const void* k_cache, const void* v_cache, int d,
-                           int page_size, int Hkv, int num_pages);
-
 // Records a description of the last host-side failure of this thread
 // (returned by ta_last_error) and returns `code`.
 ta_status fail(ta_status code, const char* where, cudaError_t err = cudaSuccess);
@@ -98,23 +92,12 @@ bool make_decode_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int p
 // SMs of the current device (148 when none can be queried).
 int current_sm_count();
 
-// The paged decode's split kernels over each sequence's keys from own_start[s]
-// on (device array), at most max_own of them.  pdl: programmatic dependent of
-// the kernel launched before.
-cudaError_t launch_decode_own(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                              const int32_t* seq_lens, const int32_t* own_start, int max_own, int page_size,
-                              int num_seqs, int Hq, int Hkv, int d, int max_pages, int num_pages_total, float scale,
-                              const DecodePlan& plan, float* part_o, float* part_lse, unsigned* status, bool pdl,
-                              cudaStream_t stream);
-
 // Plan and workspace of the shared-prefix decode (byte offsets; pure host arithmetic).
 struct SharedPlan {
-  DecodePlan own;   // splits of the keys sequences have of their own
-  int n_ctas;       // CTAs the prefix work is cut over
-  size_t groups, own_start, group_of, pre_o, pre_lse, own_o, own_lse, bytes;
+  int n_ctas;   // CTAs the work is cut over: the current device's SMs
+  size_t items, group_of, pre_o, pre_lse, own_o, own_lse, bytes;
 };
-bool make_shared_plan(int num_seqs, int num_groups, int Hq, int Hkv, int d, int max_own_len, int page_size,
-                      SharedPlan* plan);
+bool make_shared_plan(int num_seqs, int num_groups, int Hq, int Hkv, int d, SharedPlan* plan);
 
 ta_status launch_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                                const int32_t* seq_lens, const int32_t* group_offsets, const int32_t* prefix_lens,
