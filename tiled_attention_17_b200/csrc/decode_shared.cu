@@ -17,9 +17,7 @@
 // bytes for 64 sequences of about 256 own tokens, 104 us against 8 us with
 // groups of 8 heads at d = 64).
 //
-// Three kernels, each a programmatic dependent of the one before:
-//   shared_plan_kernel     one CTA: the group of each sequence, where its own
-//                          keys start, and a running count of all the work
+// Two kernels, the second a programmatic dependent of the first:
 //   shared_attend_kernel   all products, cut evenly over the SMs
 //   shared_combine_kernel  joins a row's partials by their log-sum-exp
 //
@@ -86,29 +84,29 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// One group's prefix or one sequence's own keys, as the plan kernel found it:
-// ranges checked, work counted.
-struct __align__(16) Item {
-  long long x0;   // cost of all items before it
+// One group's prefix or one sequence's own keys, ranges checked.
+struct Item {
+  long long x0;   // its place on the line of costs
   int unit0;      // units of its kind before it
   int first, n;   // first sequence, number of sequences (own keys: 1)
   int base;       // first key of its first tile (the start of a page)
-  int lo, end;    // its keys: [base + lo, end)
-};
-static_assert(sizeof(Item) == 32, "two 16-byte loads");
-
-struct PlanHeader {
-  long long total;     // cost of all items
-  long long per_cta;   // L
+  int lo, end;    // its keys: [base + lo, end); none if end <= base
+  int group;      // own keys: the group whose prefix the sequence uses, or -1
 };
 
-__host__ __device__ __forceinline__ int item_tiles(const Item& it) { return (it.end - it.base + kTile - 1) / kTile; }
-__host__ __device__ __forceinline__ int item_blocks(const Item& it, int G) {   // blocks of query rows
-  return static_cast<int>((static_cast<long long>(it.n) * G + kUnitRows - 1) / kUnitRows);
-}
-__host__ __device__ __forceinline__ int item_shift(const Item& it, int G) {   // log2 of the cost of one step
-  return it.n * G > kTile ? kWideShift : 0;
-}
+// What the combine kernel needs of the plan.
+struct __align__(16) GroupPlan {
+  long long x0;
+  int unit0, first, n, tiles, pad[2];
+};
+struct __align__(16) SeqPlan {
+  long long x0;   // of its own keys
+  int tiles, group;
+};
+
+__host__ __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
+__host__ __device__ __forceinline__ int blocks_of(int n, int G) { return (n * G + kUnitRows - 1) / kUnitRows; }   // of rows
+__host__ __device__ __forceinline__ int shift_of(int n, int G) { return n * G > kTile ? kWideShift : 0; }   // log2 cost of a step
 
 struct SharedArgs {
   const int32_t* block_table;
@@ -118,168 +116,90 @@ struct SharedArgs {
   int page_size, num_seqs, num_groups, Hq, Hkv, G, max_pages, num_pages_total, n_ctas, max_own;
   float scale, scale_log2;
   // workspace
-  unsigned* status;
-  PlanHeader* header;
-  Item* items;          // [num_groups + num_seqs + 1]: prefixes, own keys, the end of the line
-  int32_t* group_of;    // [num_seqs] group whose prefix a sequence uses, or -1
-  float* pre_o;         // [slots][D / 4][256][4] normalised prefix partials
-  float* pre_lse;       // [slots][256]
-  float* own_o;         // [slots][2][G][D] normalised partials of own keys
-  float* own_lse;       // [slots][2][G]
+  unsigned* status;       // the call's status word (written by the combine kernel)
+  unsigned* cta_status;   // [n_ctas]
+  long long* per_cta;     // cost of one CTA's share
+  GroupPlan* groups;      // [num_groups]
+  SeqPlan* seqs;          // [num_seqs]
+  float* pre_o;           // [slots][D / 4][256][4] normalised prefix partials
+  float* pre_lse;         // [slots][256]
+  float* own_o;           // [slots][2][G][D] normalised partials of own keys
+  float* own_lse;         // [slots][2][G]
 };
 
-// ---------------------------------------------------------------------------
-// Plan
-// ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
-constexpr int kStagedGroups = 1024;   // group offsets held in shared memory
-
-// A group's prefix with its ranges checked.  bad_offsets: the offsets decrease
-// or leave the batch, so groups might overlap.
-__device__ __forceinline__ Item read_group(const SharedArgs& a, int g, bool& bad_offsets, bool& bad_len) {
+// Item i: a group's prefix (i < groups) or the own keys of sequence i - groups;
+// beyond the last sequence one without keys.  x0 and unit0 are left open.
+__device__ __forceinline__ Item describe_item(const SharedArgs& a, int groups, int i, bool& bad) {
   const int cap = a.max_pages * a.page_size;
-  const int lo = __ldg(a.group_offsets + g), hi = __ldg(a.group_offsets + g + 1), len = __ldg(a.prefix_lens + g);
   Item r = {};
-  r.first = min(max(lo, 0), a.num_seqs);
-  const int last = min(max(hi, r.first), a.num_seqs);
-  r.n = last - r.first;
-  r.end = r.n > 0 ? min(max(len, 0), cap) : 0;   // a group without sequences shares nothing, whatever its length
-  bad_offsets = bad_offsets || lo != r.first || hi != last;
-  bad_len = bad_len || (r.n > 0 && len != r.end);
+  r.group = -1;
+  if (i < groups) {
+    const int len = __ldg(a.prefix_lens + i);
+    r.first = __ldg(a.group_offsets + i);
+    r.n = __ldg(a.group_offsets + i + 1) - r.first;
+    if (r.n > 0) {   // a group without sequences shares nothing, whatever its length
+      r.end = min(max(len, 0), cap);
+      bad = bad || r.end != len;
+    }
+  } else if (i - groups < a.num_seqs) {
+    const int s = i - groups, raw = __ldg(a.seq_lens + s);
+    int len = min(max(raw, 0), cap), start = 0;
+    int lo = 0, hi = groups;   // the first group whose end lies behind s
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.group_offsets + mid + 1) <= s) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo < groups && __ldg(a.group_offsets + lo) <= s) {
+      // a sequence shorter than its group's prefix does not use it: all its keys are its own
+      const int prefix = min(max(__ldg(a.prefix_lens + lo), 0), cap);
+      if (prefix > 0 && len >= prefix) {
+        start = prefix;
+        r.group = lo;
+      }
+    }
+    bad = bad || raw != len || len - start > a.max_own;
+    len = min(len, start + a.max_own);
+    r.first = s;
+    r.n = 1;
+    r.base = start & ~(a.page_size - 1);
+    r.lo = start - r.base;
+    r.end = len > start ? len : r.base;
+  }
   return r;
 }
 
-// Sums over the threads before this one (`before`), and over all (`total`).
-__device__ __forceinline__ void block_scan(long long v, int u, long long& before, int& before_u, long long& total) {
-  __shared__ long long s_v[kPlanThreads / 32];
-  __shared__ int s_u[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long sv = v;
-  int su = u;
+// 32 items, one a lane, with their costs and places: base and base_u are those of
+// the first; moved on to the next 32.  (Out of line: called from three places,
+// none of them hot.)
+struct Window {
+  Item it;
+  long long cost;
+};
+__device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int w, long long& base, int& base_u,
+                                           bool& bad) {
+  const int lane = threadIdx.x & 31, i = w * 32 + lane;
+  Window r;
+  r.it = describe_item(a, groups, i, bad);
+  const int tiles = tiles_of(r.it.end - r.it.base);
+  const int units = tiles > 0 ? blocks_of(r.it.n, a.G) * a.Hkv : 0, own_units = i < groups ? units : 0;
+  r.cost = (static_cast<long long>(units) * tiles) << shift_of(r.it.n, a.G);
+  long long sum = r.cost;
+  int sum_u = own_units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, sv, o);
-    const int y = __shfl_up_sync(0xffffffffu, su, o);
+    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+    const int y = __shfl_up_sync(0xffffffffu, sum_u, o);
     if (lane >= o) {
-      sv += x;
-      su += y;
+      sum += x;
+      sum_u += y;
     }
   }
-  __syncthreads();   // an earlier scan's sums have been read
-  if (lane == 31) {
-    s_v[warp] = sv;
-    s_u[warp] = su;
-  }
-  __syncthreads();
-  before = sv - v;
-  before_u = su - u;
-  total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) {
-      before += s_v[w];
-      before_u += s_u[w];
-    }
-    total += s_v[w];
-  }
-}
-
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
-  __shared__ int s_off[kStagedGroups + 1];
-  grid_launch_dependents();   // the attend kernel sets up meanwhile; it waits before it reads the plan
-  const int tid = threadIdx.x;
-  if (tid == 0) *a.status = 0;
-  const bool staged = a.num_groups <= kStagedGroups;
-  if (staged && a.num_groups > 0)
-    for (int g = tid; g <= a.num_groups; g += kPlanThreads) s_off[g] = __ldg(a.group_offsets + g);
-  bool bad_offsets = false, bad_len = false, seen = false;
-
-  // prefixes: each thread a contiguous run of groups
-  long long total = 0;
-  bool ignore = false;
-  if (a.num_groups > 0) {
-    const int run = (a.num_groups + kPlanThreads - 1) / kPlanThreads;
-    const int g0 = min(tid * run, a.num_groups), g1 = min(g0 + run, a.num_groups);
-    auto units_of = [&](const Item& r) { return r.end > 0 ? item_blocks(r, a.G) * a.Hkv : 0; };
-    auto cost_of = [&](const Item& r) { return (static_cast<long long>(units_of(r)) * item_tiles(r)) << item_shift(r, a.G); };
-    long long cost = 0, before;
-    int units = 0, before_u;
-    for (int g = g0; g < g1; ++g) {
-      const Item r = read_group(a, g, bad_offsets, bad_len);
-      units += units_of(r);
-      cost += cost_of(r);
-    }
-    // groups that might overlap are all left out (flagged): every sequence then reads its own row only
-    ignore = __syncthreads_or(bad_offsets);
-    block_scan(cost, units, before, before_u, total);
-    for (int g = g0; g < g1; ++g) {
-      Item r = read_group(a, g, seen, seen);
-      r.x0 = ignore ? 0 : before;
-      r.unit0 = before_u;
-      a.items[g] = r;
-      before += cost_of(r);
-      before_u += units_of(r);
-    }
-    if (ignore) total = 0;
-  }
-  __syncthreads();
-
-  // own keys: each thread a contiguous run of sequences.  A sequence shorter
-  // than its group's prefix does not use it (all its keys are its own).
-  const int run = (a.num_seqs + kPlanThreads - 1) / kPlanThreads;
-  const int s0 = min(tid * run, a.num_seqs), s1 = min(s0 + run, a.num_seqs);
-  const int cap = a.max_pages * a.page_size;
-  auto own_keys = [&](int s, int& of) {
-    const int raw = __ldg(a.seq_lens + s);
-    int len = min(max(raw, 0), cap), start = 0;
-    of = -1;
-    if (!ignore) {   // the first group whose end lies behind it
-      int lo = 0, hi = a.num_groups;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if ((staged ? s_off[mid + 1] : __ldg(a.group_offsets + mid + 1)) <= s) lo = mid + 1;
-        else hi = mid;
-      }
-      if (lo < a.num_groups && (staged ? s_off[lo] : __ldg(a.group_offsets + lo)) <= s) {
-        const int prefix = min(max(__ldg(a.prefix_lens + lo), 0), cap);
-        if (prefix > 0 && len >= prefix) {
-          start = prefix;
-          of = lo;
-        }
-      }
-    }
-    if (raw != len || len - start > a.max_own) bad_len = true;
-    len = min(len, start + a.max_own);
-    Item r = {};
-    r.unit0 = s * a.Hkv;
-    r.first = s;
-    r.n = 1;
-    r.base = start / a.page_size * a.page_size;
-    r.lo = start - r.base;
-    r.end = len > start ? len : r.base;   // no key of its own: no tile
-    return r;
-  };
-  long long cost = 0, before, own_total;
-  int unused, of;
-  for (int s = s0; s < s1; ++s) cost += static_cast<long long>(item_tiles(own_keys(s, of))) * a.Hkv;
-  block_scan(cost, 0, before, unused, own_total);
-  before += total;
-  for (int s = s0; s < s1; ++s) {
-    Item r = own_keys(s, of);
-    r.x0 = before;
-    a.items[a.num_groups + s] = r;
-    a.group_of[s] = of;
-    before += static_cast<long long>(item_tiles(r)) * a.Hkv;
-  }
-  total += own_total;
-  if (tid == 0) {
-    Item end = {};
-    end.x0 = total;
-    a.items[a.num_groups + a.num_seqs] = end;
-    a.header->total = total;
-    const long long per = (total + a.n_ctas - 1) / a.n_ctas;
-    a.header->per_cta = per < kWideCost ? kWideCost : per;   // a share holds the start of at least one step of any unit inside it
-  }
-  if (bad_offsets || bad_len) atomicOr(a.status, kDevBadSeqLen);
+  r.it.x0 = base + sum - r.cost;
+  r.it.unit0 = i < groups ? base_u + sum_u - own_units : r.it.first * a.Hkv;
+  base += __shfl_sync(0xffffffffu, sum, 31);
+  base_u += __shfl_sync(0xffffffffu, sum_u, 31);
+  return r;
 }
 
 // Steps of a unit that start in CTA c's share: [j0, j1) of `tiles`, x0 the
@@ -326,6 +246,8 @@ constexpr uint32_t kQLoads = 8;
 constexpr int kQSlots = 8, kOwnP = 64 * 128;
 constexpr int kOwnCols = 16;   // columns of the own-keys products: 8 rows of queries, and 8 that do not count
 
+constexpr int kMaxWindows = (2 * 65535 + 31) / 32;   // of 32 items
+
 template <int D>
 struct AttendLayout {
   static constexpr int kChunks = D / 64;               // 128-byte swizzle rows along d
@@ -341,12 +263,13 @@ struct AttendLayout {
   static constexpr int kRed = kSeg + kSegments * static_cast<int>(sizeof(Segment));   // [row tile][2][4 warps][8] floats
   static constexpr int kBar = kRed + 2 * 2 * 4 * 8 * 4;
   // k_full, k_empty, v_full, v_empty; per row tile: s_full, p_half, p_ready, o_free, o_done, exchange, q_full[]; segment full, empty;
-  // mma_done
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 12 + 2 * kQLoads + 2 * kSegments + 1;
-  static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag
+  // mma_done, windows read
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 12 + 2 * kQLoads + 2 * kSegments + 2;
+  static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag, status word; line's cost, CTA's share
   // slack to align the base to 1024 B; with d = 64 the own-keys product reads 64 rows it does not need, 1 KB on
-  static constexpr int kAlloc = kMisc + 16 + 1024 + (D == 64 ? 1024 : 0);
+  static constexpr int kAlloc = kMisc + 32 + 1024 + (D == 64 ? 1024 : 0);
   static_assert(kAlloc <= 232448, "shared memory of one CTA");
+  static_assert(kMaxWindows * 12 <= kKStages * kTileBytes, "the plan's windows overlay the K ring");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kTmS0 = 0, kTmS1 = 128, kTmO0 = 256, kTmO1 = 256 + D;
 };
@@ -355,7 +278,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                         const SharedArgs a) {
+                         const __grid_constant__ SharedArgs a) {
   using L = AttendLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -376,13 +299,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (12 + t * kQLoads + load % kQLoads); };
   auto BAR_GF = [&](uint32_t e) { return bar_s + 8u * e; };
   auto BAR_GE = [&](uint32_t e) { return bar_s + 8u * (kSegments + e); };
-  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments;
+  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments, BAR_GO = BAR_FIN + 8u;
   Segment* ring = reinterpret_cast<Segment*>(smem + L::kSeg);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  unsigned* status = reinterpret_cast<unsigned*>(smem + L::kMisc + 8);   // this CTA's
+  long long* line = reinterpret_cast<long long*>(smem + L::kMisc + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- setup, before the plan is needed
+  grid_launch_dependents();   // the combine kernel waits for this grid before it reads anything
+  // ---- setup
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < KS; ++s) {
       mbar_init(BAR_KF(s), 1);
@@ -406,7 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR_GE(e), 4 + 256);   // the MMA and copying warps and every softmax thread
     }
     mbar_init(BAR_FIN, 2);
+    mbar_init(BAR_GO, 1);
     *abort_flag = 0;
+    *status = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -419,53 +347,157 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
+  // ---- plan.  Every CTA counts the whole line for itself: the arrays are a few
+  // numbers a sequence, and a kernel of its own for them cost 8 us.
+  // Groups that decrease or leave the batch might overlap: then none is used.
+  bool bad = false;
+  for (int g = threadIdx.x; g < a.num_groups; g += kThreads) {
+    const int lo = __ldg(a.group_offsets + g), hi = __ldg(a.group_offsets + g + 1);
+    bad = bad || lo < 0 || hi < lo || hi > a.num_seqs;
+  }
   tc_fence_before();
+  const bool ignore = __syncthreads_or(bad);
+  const int groups = ignore ? 0 : a.num_groups, n_items = groups + a.num_seqs, n_windows = (n_items + 31) / 32;
+  long long* wx = reinterpret_cast<long long*>(smem + L::kK);   // cost, then place, of each window of 32 items
+  int* wu = reinterpret_cast<int*>(wx + kMaxWindows);
+  for (int w = warp; w < n_windows; w += kThreads / 32) {
+    long long cost = 0;
+    int units = 0;
+    load_window(a, groups, w, cost, units, bad);
+    if (lane == 0) {
+      wx[w] = cost;
+      wu[w] = units;
+    }
+  }
+  if (bad) atomicOr(status, kDevBadSeqLen);
+  __syncthreads();
+  if (warp == 0) {   // sums before each window
+    long long base = 0;
+    int base_u = 0;
+    for (int w0 = 0; w0 < n_windows; w0 += 32) {
+      const int w = w0 + lane;
+      const long long c = w < n_windows ? wx[w] : 0;
+      const int u = w < n_windows ? wu[w] : 0;
+      long long sum = c;
+      int sum_u = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+        const int y = __shfl_up_sync(0xffffffffu, sum_u, o);
+        if (lane >= o) {
+          sum += x;
+          sum_u += y;
+        }
+      }
+      if (w < n_windows) {
+        wx[w] = base + sum - c;
+        wu[w] = base_u + sum_u - u;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      base_u += __shfl_sync(0xffffffffu, sum_u, 31);
+    }
+    if (lane == 0) {
+      long long per = base <= UINT32_MAX - a.n_ctas
+                          ? (static_cast<unsigned>(base) + a.n_ctas - 1) / static_cast<unsigned>(a.n_ctas)
+                          : (base + a.n_ctas - 1) / a.n_ctas;
+      if (per < kWideCost) per = kWideCost;   // a share inside a unit holds the start of a step at least
+      line[0] = base;
+      line[1] = per;
+      if (blockIdx.x == 0) *a.per_cta = per;
+    }
+  }
+  fence_proxy_async_smem();   // the windows' memory becomes the K ring
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const long long per = line[1];
+  if (warp == kThreads / 32 - 2) {
+    // The combine kernel's tables, 32 items of them by every n_ctas-th CTA (lane k
+    // holds the place of the CTA's k-th window; read before the K ring fills).
+    const int mine = static_cast<int>(blockIdx.x) + lane * a.n_ctas;
+    const long long at = mine < n_windows ? wx[mine] : 0;
+    const int at_u = mine < n_windows ? wu[mine] : 0;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR_GO);
+    __syncwarp();
+    for (int k = 0, w = static_cast<int>(blockIdx.x); w < n_windows; ++k, w += a.n_ctas) {
+      long long base = __shfl_sync(0xffffffffu, at, k);
+      int base_u = __shfl_sync(0xffffffffu, at_u, k);
+      const Item it = load_window(a, groups, w, base, base_u, bad).it;
+      const int i = w * 32 + lane, tiles = tiles_of(it.end - it.base);
+      if (i < groups) {
+        const GroupPlan g = {it.x0, it.unit0, it.first, it.n, tiles, {0, 0}};
+        a.groups[i] = g;
+      } else if (i < n_items) {
+        const SeqPlan q = {it.x0, tiles, it.group};
+        a.seqs[it.first] = q;
+      }
+    }
+  }
 
   if (warp < kSoftmaxWarp0 || warp == kMmaWarp1) {
     if (warp == 0) {
       // ======================= planner: describes the CTA's segments, up to kSegments ahead =======================
-      grid_wait();                // the plan is complete
-      grid_launch_dependents();
-      const long long per = a.header->per_cta;
-      const long long begin = per * blockIdx.x, end = min(a.header->total, begin + per);
-      const int n_items = a.num_groups + a.num_seqs, per_tile = kTile / a.page_size;
-      // where the walk is: item, unit of it, and the unit's place on the line
-      int item = 0, unit = 0, tiles = 0, blocks = 1, shift = 0;
-      long long ux = 0;
+      const long long begin = per * blockIdx.x, end = min(line[0], begin + per);
+      const int per_tile = kTile / a.page_size;
+      // where the walk is: window of items (one a lane, `work` those left in it), item, unit of it and the unit's place
+      int w = 0, base_u = 0;
+      long long base = 0;
+      Window win = {};
       Item it = {};
-      auto enter = [&](int at) {   // the first item from `at` on that has work
-        for (item = at; item < n_items; ++item) {
-          it = a.items[item];
-          tiles = item_tiles(it);
-          if (tiles > 0 && it.n > 0 && a.items[item + 1].x0 > it.x0) break;
-        }
-        blocks = item_blocks(it, a.G);
-        shift = item_shift(it, a.G);
+      uint32_t work = 0;
+      int unit = 0, tiles = 0, blocks = 1, shift = 0;
+      bool own = false;
+      long long ux = end;
+      auto enter = [&](int lane_of) {   // the item of a lane of the window
+        it.x0 = __shfl_sync(0xffffffffu, win.it.x0, lane_of);
+        it.unit0 = __shfl_sync(0xffffffffu, win.it.unit0, lane_of);
+        it.first = __shfl_sync(0xffffffffu, win.it.first, lane_of);
+        it.n = __shfl_sync(0xffffffffu, win.it.n, lane_of);
+        it.base = __shfl_sync(0xffffffffu, win.it.base, lane_of);
+        it.lo = __shfl_sync(0xffffffffu, win.it.lo, lane_of);
+        it.end = __shfl_sync(0xffffffffu, win.it.end, lane_of);
+        work &= ~((2u << lane_of) - 1u);   // items behind it
+        own = w * 32 + lane_of >= groups;
+        tiles = tiles_of(it.end - it.base);
+        blocks = blocks_of(it.n, a.G);
+        shift = shift_of(it.n, a.G);
         unit = 0;
         ux = it.x0;
       };
-      if (begin < end) {   // the last item that starts at or before `begin` owns it: a 32-way search
-        int lo = 0, n = n_items;
+      auto next_window = [&]() {
+        win = load_window(a, groups, w, base, base_u, bad);
+        work = __ballot_sync(0xffffffffu, win.cost > 0);
+      };
+      if (begin < end) {
+        int lo = 0, n = n_windows;   // the last window that starts at or before `begin`: a 32-way search
         while (n > 1) {
           const int step = (n + 31) / 32, at = lane * step;
-          const uint32_t le = __ballot_sync(0xffffffffu, at < n && a.items[lo + at].x0 <= begin);
-          const int k = 31 - __clz(le);   // items start in order, and the first does at or before `begin`
+          const uint32_t le = __ballot_sync(0xffffffffu, at < n && wx[lo + at] <= begin);
+          const int k = 31 - __clz(le);
           lo += k * step;
           n = min(step, n - k * step);
         }
-        enter(lo);
-        const long long unit_cost = static_cast<long long>(tiles) << shift;
-        unit = static_cast<int>((begin - ux) / unit_cost);
+        w = lo;
+        base = wx[w];
+        base_u = wu[w];
+        next_window();
+        // and in it the last item with work that does
+        enter(31 - __clz(__ballot_sync(0xffffffffu, win.cost > 0 && win.it.x0 <= begin)));
+        const long long unit_cost = static_cast<long long>(tiles) << shift, in = begin - ux;
+        unit = static_cast<int>(in <= UINT32_MAX ? static_cast<unsigned>(in) / static_cast<unsigned>(unit_cost) : in / unit_cost);
         ux += unit * unit_cost;
-      } else {
-        ux = end;
       }
       auto advance = [&]() {   // to the next unit, if the share reaches it
         ux += static_cast<long long>(tiles) << shift;
-        if (ux < end && ++unit == blocks * a.Hkv) enter(item + 1);
+        if (ux < end && ++unit == blocks * a.Hkv) {
+          while (work == 0) {
+            ++w;
+            next_window();
+          }
+          enter(__ffs(work) - 1);
+        }
       };
       uint32_t g0 = 0;
       int turn = 0;   // row tile that takes the next narrow step
@@ -481,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pg = -1;
         if (!done) {
           const int row0 = unit % blocks * kUnitRows;
-          const bool own = item >= a.num_groups;
+          const bool is_own = own;   // advance() moves on
           sg.g0 = g0;
           sg.tiles = j1 - j0;
           sg.rows = min(kUnitRows, it.n * a.G - row0);
@@ -490,24 +522,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           sg.lo = j0 == 0 ? it.lo : 0;
           sg.hi = it.end - it.base - j0 * kTile;
           const int slot = static_cast<int>(blockIdx.x) + it.unit0 + unit;
-          sg.slot = own ? ~slot : slot;
+          sg.slot = is_own ? ~slot : slot;
           sg.hkv = unit / blocks;
           sg.seq = it.first + row0 / a.G;
           sg.row = it.first;
           sg.page0 = it.base / a.page_size + j0 * per_tile;
-          sg.qslot = own ? static_cast<int>(n % kQSlots) : 0;
+          sg.qslot = is_own ? static_cast<int>(n % kQSlots) : 0;
           g0 += sg.tiles;
           if (!sg.wide) turn ^= sg.tiles & 1;
           const bool mine = lane < per_tile && lane * a.page_size < sg.hi;
           if (mine) pg = __ldg(a.block_table + static_cast<size_t>(sg.row) * a.max_pages + sg.page0 + lane);
           advance();   // while the table entries are under way
           if (mine && (pg < 0 || pg >= a.num_pages_total)) {   // read as page 0, flagged
-            atomicOr(a.status, kDevBadBlockTable);
+            atomicOr(status, kDevBadBlockTable);
             pg = 0;
           }
         }
         const uint32_t e = n % kSegments;
-        if (n >= kSegments && !wait_all(BAR_GE(e), (n / kSegments - 1) & 1u, a.status, abort_flag)) break;
+        if (n >= kSegments && !wait_all(BAR_GE(e), (n / kSegments - 1) & 1u, status, abort_flag)) break;
+        if (n == 0) {
+          fence_proxy_async_smem();   // this warp's reads of the windows, before copies into the K ring
+          if (!wait_all(BAR_GO, 0, status, abort_flag)) break;
+        }
         if (lane < kTile / 8) ring[e].pages[lane] = pg;
         if (lane == 0) {
           const int4* src = reinterpret_cast<const int4*>(&sg);
@@ -536,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
-        if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, a.status, abort_flag))) break;
+        if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, status, abort_flag))) break;
         const Segment& sg = ring[e];
         const int tiles = sg.tiles, hkv = sg.hkv, hi = sg.hi, seq = sg.seq, wide = sg.wide, tile_first = sg.tile_first;
         const uint32_t g0 = sg.g0;
@@ -553,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // A whole tile, or rows after one, wait until the scores of the last step that reads the buffer are formed:
           // where that step's K slot has not been waited for since, its release says so.
           if (qn[t] > 0 && !(own && qown[t]) && qlast[t] + KS >= g0 &&
-              !(ok = wait_all(BAR_KE(qlast[t] % KS), (qlast[t] / KS) & 1u, a.status, abort_flag)))
+              !(ok = wait_all(BAR_KE(qlast[t] % KS), (qlast[t] / KS) & 1u, status, abort_flag)))
             break;
           const uint32_t bar = BAR_QF(t, qn[t]);
           ++qn[t];
@@ -581,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int p = (j + 1) * per_tile + lane;
           const bool more = j + 1 < tiles && lane < per_tile && static_cast<long long>(p) * a.page_size < hi;
           if (more) pg_next = __ldg(row + p);
-          if (!(ok = wait_all(empty0 + 8u * slot, (use & 1u) ^ 1u, a.status, abort_flag))) break;
+          if (!(ok = wait_all(empty0 + 8u * slot, (use & 1u) ^ 1u, status, abort_flag))) break;
           const uint32_t bar = full0 + 8u * slot;
           const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(live)) * page_bytes);
@@ -595,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++use;
           }
           if (more && (pg_next < 0 || pg_next >= a.num_pages_total)) {   // read as page 0, flagged
-            atomicOr(a.status, kDevBadBlockTable);
+            atomicOr(status, kDevBadBlockTable);
             pg_next = 0;
           }
           pg = pg_next;
@@ -634,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t steps_t = 0, used = 0;   // steps and segments of this row tile: S/P and Q/O barrier phases
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
-        if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, a.status, abort_flag))) break;
+        if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, status, abort_flag))) break;
         // broadcasts tell the compiler that the values are the same in all lanes: the
         // descriptors made of them stay in uniform registers
         const uint32_t g0 = __shfl_sync(0xffffffffu, ring[e].g0, 0);
@@ -647,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tiles == 0) break;
         const int stride = wide ? 1 : 2, first = wide ? 0 : (t ^ tile_first) & 1;
         if (first >= tiles) continue;
-        if (!(ok = wait_all(BAR_QF(t, used), (used / kQLoads) & 1u, a.status, abort_flag))) break;
+        if (!(ok = wait_all(BAR_QF(t, used), (used / kQLoads) & 1u, status, abort_flag))) break;
         if (own) {
           // Few query rows: the products are taken with keys (S^T = K Q^T) and columns of
           // d (O^T = V^T P^T) on the tensor memory's lanes and the queries on its columns.
@@ -661,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, kOwnCols, false) | (1u << 15);   // A is d-major
           for (int j = first; j < tiles; j += stride, ++steps_t) {
             const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
-            if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, a.status, abort_flag))) break;
+            if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, status, abort_flag))) break;
             tc_fence_after();
             if (leader) {
               uint64_t a0 = dK + ks * kTileStep, b0 = dQ1;
@@ -676,9 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(BAR_KE(ks));
             }
             __syncwarp();
-            if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, a.status, abort_flag))) break;
-            if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, a.status, abort_flag))) break;
-            if (!(ok = wait_all(BAR_PR(t), steps_t & 1u, a.status, abort_flag))) break;
+            if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, status, abort_flag))) break;
+            if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, status, abort_flag))) break;
+            if (!(ok = wait_all(BAR_PR(t), steps_t & 1u, status, abort_flag))) break;
             tc_fence_after();
             if (leader) {
               const uint64_t a0 = dVt + vs * kTileStep;
@@ -701,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
           // S_t = Q_t K^T, 16 columns of d a step.  (The issue loops are rolled: a turn
           // takes about the 64 cycles of its MMA, and the code stays small.)
-          if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, a.status, abort_flag))) break;
+          if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, status, abort_flag))) break;
           tc_fence_after();
           if (leader) {
             uint64_t a0 = dQ, b0 = dK + ks * kTileStep;
@@ -718,11 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           // O_t += P_t V, 64 keys as soon as their weights are written.  The first of a
           // segment overwrites O_t: the epilogue before must have read it.
-          if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, a.status, abort_flag))) break;
-          if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, a.status, abort_flag))) break;
+          if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, status, abort_flag))) break;
+          if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, status, abort_flag))) break;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {   // BAR_PH(t), then BAR_PR(t)
-            if (!(ok = wait_all(BAR_PH(t) + 16u * half, steps_t & 1u, a.status, abort_flag))) break;
+            if (!(ok = wait_all(BAR_PH(t) + 16u * half, steps_t & 1u, status, abort_flag))) break;
             tc_fence_after();
             if (leader) {
               const uint64_t b0 = dV + vs * kTileStep;
@@ -761,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t steps_t = 0, held = 0, exchanges = 0;   // S/P and O barrier phases of this row tile
     for (uint32_t seg = 0; ok; ++seg) {
       const uint32_t e = seg % kSegments;
-      ok = wait_all(BAR_GF(e), (seg / kSegments) & 1u, a.status, abort_flag);
+      ok = wait_all(BAR_GF(e), (seg / kSegments) & 1u, status, abort_flag);
       if (!ok) break;
       const Segment sg = ring[e];
       mbar_arrive(BAR_GE(e));
@@ -779,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both row tiles' warps, each before its own product).
       auto zero_values = [&](int j, int lo, int lim) {
         const uint32_t gj = sg.g0 + static_cast<uint32_t>(j), sv = gj % VS;
-        if (!wait_all(BAR_VF(sv), (gj / VS) & 1u, a.status, abort_flag)) return false;
+        if (!wait_all(BAR_VF(sv), (gj / VS) & 1u, status, abort_flag)) return false;
         if (lane_row >= lim || lane_row < lo) {
           const int pr = lane_row % a.page_size;
           uint8_t* base = smem + L::kV + sv * L::kTileBytes + (lane_row - pr) * D * 2 + pr * 128;
@@ -810,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             reinterpret_cast<float4*>(buf + quarter * kG)[1] = make_float4(v[4], v[5], v[6], v[7]);
             mbar_arrive(BAR_X(t));
           }
-          if (!wait_all(BAR_X(t), exchanges++ & 1u, a.status, abort_flag)) return false;
+          if (!wait_all(BAR_X(t), exchanges++ & 1u, status, abort_flag)) return false;
 #pragma unroll
           for (int i = 0; i < kG; i += 4) {
             float4 x = *reinterpret_cast<const float4*>(buf + i);
@@ -828,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint8_t* prow = smem + L::kQ + t * L::kTileBytes + kOwnP + (lane_row >> 6) * (kOwnCols * 128);
         for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t) {
-          ok = wait_all(BAR_SF(t), steps_t & 1u, a.status, abort_flag);
+          ok = wait_all(BAR_SF(t), steps_t & 1u, status, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
@@ -883,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kG; ++i)
 #pragma unroll
           for (int x = 16; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-        ok = exchange(l, [](float x, float y) { return x + y; }) && wait_all(BAR_OD(t), held & 1u, a.status, abort_flag);
+        ok = exchange(l, [](float x, float y) { return x + y; }) && wait_all(BAR_OD(t), held & 1u, status, abort_flag);
         tc_fence_after();
         if (!ok) break;
         ++held;
@@ -898,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i < G) {
             const float inv = l[i] > 0.f ? __fdividef(1.f, l[i]) : 0.f;
             if (lane_row < D) a.own_o[(at + i) * D + lane_row] = __uint_as_float(orr[i]) * inv;
+            if (lane_row == i && sg.tiles == 1) a.own_lse[(at ^ G) + i] = -INFINITY;   // the unit's other partial is none
             if (lane_row == i)
               a.own_lse[at + i] = l[i] > 0.f ? fmaf(m[i], a.scale, __log2f(l[i]) * 0.69314718055994531f) : -INFINITY;
           }
@@ -905,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t) {
-        ok = wait_all(BAR_SF(t), steps_t & 1u, a.status, abort_flag);
+        ok = wait_all(BAR_SF(t), steps_t & 1u, status, abort_flag);
         if (!ok) break;
         tc_fence_after();
         // keys of this tile: columns [lo, lim); the rest of its shared memory holds none that count
@@ -999,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the partial: O / l and m scale + ln l, in fp32
-      ok = wait_all(BAR_OD(t), held & 1u, a.status, abort_flag);
+      ok = wait_all(BAR_OD(t), held & 1u, status, abort_flag);
       tc_fence_after();
       if (!ok) break;
       ++held;
@@ -1022,6 +1059,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (live) {
+          if (!sg.wide && sg.tiles == 1)   // the unit's other partial is none
+            a.pre_lse[slot * kUnitRows + (half ^ 1) * kTile + row] = -INFINITY;
           a.pre_lse[slot * kUnitRows + half * kTile + row] =
               (l > 0.f) ? fmaf(m, a.scale, __log2f(l) * 0.69314718055994531f) : -INFINITY;
         }
@@ -1034,6 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- teardown
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) a.cta_status[blockIdx.x] = *status;
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -1046,12 +1086,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // partial of columns [4 c4, 4 c4 + 4) of query head g, the NP runs meet in
 // shared memory.  Weights e^(lse_i - max) over all partials of a row.
 // ---------------------------------------------------------------------------
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 512;
 
+__device__ __forceinline__ long long divide(long long x, long long y) {   // both >= 0; in 32 bits where it fits
+  return ((x | y) >> 32) == 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(y) : x / y;
+}
 // The CTAs [c0, c0 + n) that hold partials of a unit at place x0 on the line.
-__device__ __forceinline__ void unit_ctas(long long x0, int tiles, int shift, long long per, long long& c0, int& n) {
-  c0 = x0 / per;
-  n = static_cast<int>((x0 + (static_cast<long long>(tiles - 1) << shift)) / per - c0) + 1;
+__device__ __forceinline__ void unit_ctas(long long x0, int tiles, int shift, long long per, int& c0, int& n) {
+  c0 = static_cast<int>(divide(x0, per));
+  n = static_cast<int>(divide(x0 + (static_cast<long long>(tiles - 1) << shift), per)) - c0 + 1;
 }
 
 template <int D, int G>
@@ -1064,71 +1107,87 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
   const int hkv = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
   const int p0 = tid / kPer, c4 = (tid % kPer) / G, gq = tid % G;
   grid_wait();   // the partials are complete
-  const long long per = a.header->per_cta;
+  const SeqPlan sp = a.seqs[seq];
+  const long long per = *a.per_cta;
+  // partials of the prefix (n_pre of them, `pre_step` floats apart; narrow rows have two a slot) and of the own keys
+  int n_pre = 0, n_own = 0;
+  size_t pre0 = 0, own0 = 0;
+  bool wide = true;
+  if (sp.group >= 0) {
+    const GroupPlan g = a.groups[sp.group];
+    const int blocks = blocks_of(g.n, G), shift = shift_of(g.n, G);
+    const int r = (seq - g.first) * G, block = r / kUnitRows, unit = hkv * blocks + block;
+    wide = min(kUnitRows, g.n * G - block * kUnitRows) > kTile;
+    int c0;
+    unit_ctas(g.x0 + ((static_cast<long long>(unit) * g.tiles) << shift), g.tiles, shift, per, c0, n_pre);
+    pre0 = static_cast<size_t>(c0 + g.unit0 + unit) * kUnitRows + r % kUnitRows + gq;
+    if (!wide) n_pre *= 2;
+  }
+  if (sp.tiles > 0) {
+    int c0;
+    unit_ctas(sp.x0 + static_cast<long long>(hkv) * sp.tiles, sp.tiles, 0, per, c0, n_own);
+    own0 = static_cast<size_t>(c0 + seq * a.Hkv + hkv) * 2 * G + gq;
+    n_own *= 2;
+  }
+  const int n = n_pre + n_own;
+  auto place = [&](int i, const float*& w, const float4*& v) {
+    if (i < n_pre) {
+      const size_t row = pre0 + static_cast<size_t>(wide ? i * kUnitRows : i * kTile);   // two halves of 128 rows a slot
+      w = a.pre_lse + row;
+      v = reinterpret_cast<const float4*>(a.pre_o) + (row / kUnitRows * (D / 4) + c4) * kUnitRows + row % kUnitRows;
+    } else {
+      const size_t row = own0 + static_cast<size_t>(i - n_pre) * G;
+      w = a.own_lse + row;
+      v = reinterpret_cast<const float4*>(a.own_o) + row * (D / 4) + c4;
+    }
+  };
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto join = [&](float w, const float4& v) {
-    if (w == -INFINITY) return;
-    const float mn = fmaxf(m, w), s0 = __expf(m - mn), s1 = __expf(w - mn);
-    l = fmaf(l, s0, s1);
-    acc.x = fmaf(acc.x, s0, s1 * v.x);
-    acc.y = fmaf(acc.y, s0, s1 * v.y);
-    acc.z = fmaf(acc.z, s0, s1 * v.z);
-    acc.w = fmaf(acc.w, s0, s1 * v.w);
+  constexpr int kAhead = 4;   // partials loaded before the first is joined
+  for (int i0 = p0; i0 < n; i0 += kAhead * NP) {
+    float w[kAhead];
+    float4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      w[k] = -INFINITY;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + k * NP < n) {
+        const float* pw;
+        const float4* pv;
+        place(i0 + k * NP, pw, pv);
+        w[k] = *pw;
+        v[k] = *pv;
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, w[k]);
+    if (mn == -INFINITY) continue;
+    const float s0 = __expf(m - mn);
     m = mn;
-  };
-  // A narrow segment of two or more steps made two partials, one of a single step one.
-  const int of = a.group_of[seq];
-  if (of >= 0) {
-    const Item it = a.items[of];
-    const int tiles = item_tiles(it), blocks = item_blocks(it, G), shift = item_shift(it, G);
-    const int r = (seq - it.first) * G + gq, block = r / kUnitRows, unit = hkv * blocks + block;
-    const int urow = r % kUnitRows;
-    const bool wide = min(kUnitRows, it.n * G - block * kUnitRows) > kTile;
-    const long long x0 = it.x0 + ((static_cast<long long>(unit) * tiles) << shift);
-    long long c0;
-    int n;
-    unit_ctas(x0, tiles, shift, per, c0, n);
-    const size_t slot0 = static_cast<size_t>(c0) + it.unit0 + unit;
-#pragma unroll 4
-    for (int i = p0; i < (wide ? n : 2 * n); i += NP) {
-      const int k = wide ? i : i >> 1, h = wide ? 0 : i & 1;
-      if (h) {
-        int j0, j1;
-        unit_share(x0, tiles, shift, per, static_cast<int>(c0) + k, j0, j1);
-        if (j1 - j0 < 2) continue;
+    l *= s0;
+    acc = make_float4(acc.x * s0, acc.y * s0, acc.z * s0, acc.w * s0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (w[k] != -INFINITY) {   // an empty partial's values may be anything
+        const float s1 = __expf(w[k] - mn);
+        l += s1;
+        acc.x = fmaf(s1, v[k].x, acc.x);
+        acc.y = fmaf(s1, v[k].y, acc.y);
+        acc.z = fmaf(s1, v[k].z, acc.z);
+        acc.w = fmaf(s1, v[k].w, acc.w);
       }
-      const size_t at = (slot0 + k) * kUnitRows + h * kTile + urow;
-      join(a.pre_lse[at], reinterpret_cast<const float4*>(a.pre_o)[(slot0 + k) * (D / 4) * kUnitRows +
-                                                                  static_cast<size_t>(c4) * kUnitRows + h * kTile + urow]);
-    }
-  }
-  {
-    const Item it = a.items[a.num_groups + seq];
-    const int tiles = item_tiles(it);
-    if (tiles > 0) {
-      const long long x0 = it.x0 + static_cast<long long>(hkv) * tiles;
-      long long c0;
-      int n;
-      unit_ctas(x0, tiles, 0, per, c0, n);
-      const size_t slot0 = static_cast<size_t>(c0) + it.unit0 + hkv;
-#pragma unroll 4
-      for (int i = p0; i < 2 * n; i += NP) {
-        const int k = i >> 1, h = i & 1;
-        if (h) {
-          int j0, j1;
-          unit_share(x0, tiles, 0, per, static_cast<int>(c0) + k, j0, j1);
-          if (j1 - j0 < 2) continue;
-        }
-        const size_t at = ((slot0 + k) * 2 + h) * G + gq;
-        join(a.own_lse[at], reinterpret_cast<const float4*>(a.own_o)[at * (D / 4) + c4]);
-      }
-    }
   }
   s_m[tid] = m;
   s_l[tid] = l;
   s_o[tid] = acc;
   __syncthreads();
+  if (hkv == 0 && seq == 0 && tid < 32) {   // the call's status: any CTA's
+    unsigned bits = 0;
+    for (int c = tid; c < a.n_ctas; c += 32) bits |= a.cta_status[c];
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (tid == 0) *a.status = bits;
+  }
   if (p0 != 0) return;
   float M = m;
   for (int p = 1; p < NP; ++p) M = fmaxf(M, s_m[p * kPer + tid]);
@@ -1206,7 +1265,7 @@ ta_status launch_attend(const void* q, const void* k_cache, const void* v_cache,
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_limit(shared_attend_kernel<D>, L::kAlloc, attr_done);
   if (e != cudaSuccess) return fail(TA_ERR_CUDA, "shared decode: shared-memory limit", e);
-  e = launch(shared_attend_kernel<D>, dim3(static_cast<unsigned>(a.n_ctas)), kThreads, L::kAlloc, true, stream, tq, tq1,
+  e = launch(shared_attend_kernel<D>, dim3(static_cast<unsigned>(a.n_ctas)), kThreads, L::kAlloc, false, stream, tq, tq1,
              tk, tv, a);
   return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: attend kernel launch", e);
 }
@@ -1235,14 +1294,16 @@ bool make_shared_plan(int num_seqs, int num_groups, int Hq, int Hkv, int d, Shar
   const long long slots = units == 0 ? 0 : units + p->n_ctas;
   const long long own_slots = static_cast<long long>(num_seqs) * Hkv + p->n_ctas;
   if (slots > INT32_MAX || own_slots > INT32_MAX) return false;
-  size_t at = 512;   // status word, plan header
+  if (p->n_ctas < (kMaxWindows + 31) / 32 && (num_groups + num_seqs + 31) / 32 > 32 * p->n_ctas) return false;
+  size_t at = 256;   // status word, a CTA's share
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = up256(at + bytes);
     return here;
   };
-  p->items = take((static_cast<size_t>(num_groups) + num_seqs + 1) * sizeof(Item));
-  p->group_of = take(static_cast<size_t>(num_seqs) * 4);
+  p->cta_status = take(static_cast<size_t>(p->n_ctas) * 4);
+  p->groups = take(static_cast<size_t>(num_groups) * sizeof(GroupPlan));
+  p->seqs = take(static_cast<size_t>(num_seqs) * sizeof(SeqPlan));
   p->pre_o = take(static_cast<size_t>(slots) * kUnitRows * d * 4);
   p->pre_lse = take(static_cast<size_t>(slots) * kUnitRows * 4);
   p->own_o = take(static_cast<size_t>(own_slots) * 2 * G * d * 4);
@@ -1277,21 +1338,20 @@ ta_status launch_decode_shared(const void* q, const void* k_cache, const void* v
   // 0 times that would be NaN
   a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1e-30f);
   a.status = reinterpret_cast<unsigned*>(ws);
-  a.header = reinterpret_cast<PlanHeader*>(ws + 256);
-  a.items = reinterpret_cast<Item*>(ws + plan.items);
-  a.group_of = reinterpret_cast<int32_t*>(ws + plan.group_of);
+  a.per_cta = reinterpret_cast<long long*>(ws + 128);
+  a.cta_status = reinterpret_cast<unsigned*>(ws + plan.cta_status);
+  a.groups = reinterpret_cast<GroupPlan*>(ws + plan.groups);
+  a.seqs = reinterpret_cast<SeqPlan*>(ws + plan.seqs);
   a.pre_o = reinterpret_cast<float*>(ws + plan.pre_o);
   a.pre_lse = reinterpret_cast<float*>(ws + plan.pre_lse);
   a.own_o = reinterpret_cast<float*>(ws + plan.own_o);
   a.own_lse = reinterpret_cast<float*>(ws + plan.own_lse);
 
-  cudaError_t e = launch(shared_plan_kernel, dim3(1), kPlanThreads, 0, false, stream, a);
-  if (e != cudaSuccess) return fail(TA_ERR_CUDA, "shared decode: plan kernel launch", e);
   const ta_status st = d == 128 ? launch_attend<128>(q, k_cache, v_cache, a, stream)
                                 : launch_attend<64>(q, k_cache, v_cache, a, stream);
   if (st != TA_OK) return st;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(o);
-  e = d == 128 ? launch_combine<128>(a, out, lse, stream) : launch_combine<64>(a, out, lse, stream);
+  const cudaError_t e = d == 128 ? launch_combine<128>(a, out, lse, stream) : launch_combine<64>(a, out, lse, stream);
   return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: combine kernel launch", e);
 }
 

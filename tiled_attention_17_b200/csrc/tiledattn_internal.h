@@ -95,7 +95,7 @@ int current_sm_count();
 // Plan and workspace of the shared-prefix decode (byte offsets; pure host arithmetic).
 struct SharedPlan {
   int n_ctas;   // CTAs the work is cut over: the current device's SMs
-  size_t items, group_of, pre_o, pre_lse, own_o, own_lse, bytes;
+  size_t cta_status, groups, seqs, pre_o, pre_lse, own_o, own_lse, bytes;
 };
 bool make_shared_plan(int num_seqs, int num_groups, int Hq, int Hkv, int d, SharedPlan* plan);
 
