@@ -241,9 +241,9 @@ constexpr int kSegments = 4;   // ring depth
 constexpr uint32_t kQLoads = 8;
 // Own keys have at most 8 query rows.  Their loads go round 8 places of 8 rows in
 // the first half of a query buffer, so the loads of the next segments need not
-// wait for the products of this one; the second half takes the weights of the
-// step (prefixes come first on the line, so no whole query tile follows).
-constexpr int kQSlots = 8, kOwnP = 64 * 128;
+// wait for the products of this one; the second half takes the weights of two
+// steps (prefixes come first on the line, so no whole query tile follows).
+constexpr int kQSlots = 8, kOwnP = 64 * 128, kOwnPBytes = 4096;
 constexpr int kOwnCols = 16;   // columns of the own-keys products: 8 rows of queries, and 8 that do not count
 
 constexpr int kMaxWindows = (2 * 65535 + 31) / 32;   // of 32 items
@@ -262,9 +262,9 @@ struct AttendLayout {
   static constexpr int kSeg = kV + kVStages * kTileBytes;
   static constexpr int kRed = kSeg + kSegments * static_cast<int>(sizeof(Segment));   // [row tile][2][4 warps][8] floats
   static constexpr int kBar = kRed + 2 * 2 * 4 * 8 * 4;
-  // k_full, k_empty, v_full, v_empty; per row tile: s_full, p_half, p_ready, o_free, o_done, exchange, q_full[]; segment full, empty;
-  // mma_done, windows read
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 12 + 2 * kQLoads + 2 * kSegments + 2;
+  // k_full, k_empty, v_full, v_empty; per row tile: s_full, p_half, p_ready, o_free, o_done, exchange, own s_full[2], q_full[]; segment full, empty;
+  // mma_done, windows read, staggered start
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 16 + 2 * kQLoads + 2 * kSegments + 3;
   static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag, status word; line's cost, CTA's share
   // slack to align the base to 1024 B; with d = 64 the own-keys product reads 64 rows it does not need, 1 KB on
   static constexpr int kAlloc = kMisc + 32 + 1024 + (D == 64 ? 1024 : 0);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
   constexpr uint32_t KS = L::kKStages, VS = L::kVStages;
-  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (12 + 2 * kQLoads);
+  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (16 + 2 * kQLoads);
   auto BAR_KF = [&](uint32_t s) { return bar0 + 8u * s; };
   auto BAR_KE = [&](uint32_t s) { return bar0 + 8u * (KS + s); };
   auto BAR_VF = [&](uint32_t s) { return bar0 + 8u * (2 * KS + s); };
@@ -296,10 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto BAR_OF = [&](int t) { return bar_t + 8u * (6 + t); };
   auto BAR_OD = [&](int t) { return bar_t + 8u * (8 + t); };
   auto BAR_X = [&](int t) { return bar_t + 8u * (10 + t); };
-  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (12 + t * kQLoads + load % kQLoads); };
+  auto BAR_SO = [&](int t, uint32_t k) { return bar_t + 8u * (12 + 2 * t + (k & 1u)); };
+  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (16 + t * kQLoads + load % kQLoads); };
   auto BAR_GF = [&](uint32_t e) { return bar_s + 8u * e; };
   auto BAR_GE = [&](uint32_t e) { return bar_s + 8u * (kSegments + e); };
-  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments, BAR_GO = BAR_FIN + 8u;
+  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments, BAR_GO = BAR_FIN + 8u, BAR_ST = BAR_FIN + 16u;
   Segment* ring = reinterpret_cast<Segment*>(smem + L::kSeg);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -326,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR_OF(t), 128);
       mbar_init(BAR_OD(t), 1);
       mbar_init(BAR_X(t), 4);   // one lane of each softmax warp
+      mbar_init(BAR_SO(t, 0), 1);
+      mbar_init(BAR_SO(t, 1), 1);
     }
     for (uint32_t e = 0; e < kSegments; ++e) {
       mbar_init(BAR_GF(e), 1);
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(BAR_FIN, 2);
     mbar_init(BAR_GO, 1);
+    mbar_init(BAR_ST, 4);   // one lane of each softmax warp of row tile 0
     *abort_flag = 0;
     *status = 0;
     fence_mbar_init();
@@ -667,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // page-major V: 16-key step kk starts at byte 2048 (kk + (kk & vmask))
       const int vmask = ~(max(ps / 16, 1) - 1);
       bool ok = true;
+      uint32_t wides = 0;
       uint32_t steps_t = 0, used = 0;   // steps and segments of this row tile: S/P and Q/O barrier phases
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
@@ -689,50 +694,86 @@ __global__ void __launch_bounds__(kThreads, 1)
           // d (O^T = V^T P^T) on the tensor memory's lanes and the queries on its columns.
           // Every softmax thread then has one key and a handful of weights, and
           // the products are an eighth as wide.  P^T comes from shared memory.
-          const uint64_t dQ1 = dQ + static_cast<uint64_t>(qslot * 64);
           const uint64_t dP = smem_desc_sw128(sQ + t * L::kTileBytes + kOwnP, 16, 1024);
           // with d = 64 rows 64..127 of V^T repeat others and are not read back
           const uint64_t dVt = kTwo ? dV : smem_desc_sw128(sV, 1024, 1024);
           constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kOwnCols, false);
           constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, kOwnCols, false) | (1u << 15);   // A is d-major
-          for (int j = first; j < tiles; j += stride, ++steps_t) {
-            const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
-            if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, status, abort_flag))) break;
-            tc_fence_after();
-            if (leader) {
-              uint64_t a0 = dK + ks * kTileStep, b0 = dQ1;
-#pragma unroll 1
-              for (int k = 0; k < D / 16; ++k) {
-                mma_ss(tS, a0, b0, idesc_s, k != 0 ? 1u : 0u);
-                a0 += (k & 3) == 3 ? (1024 >> 4) - 6 : 2;
-                b0 += (k & 3) == 3 ? (L::kChunkBytes >> 4) - 6 : 2;
+          // Scores run one step ahead of the products with V, into the next segments (two
+          // places for S^T and P^T), so the softmax finds its scores ready.
+          uint32_t gs = g0, k = 0, pg = 0, pused = 0;   // segment's ring position; steps; the due product's step and segment
+          int j = first, left = tiles;
+          uint64_t dQs = dQ + static_cast<uint64_t>(qslot * 64);
+          bool sfirst = true, pfirst = false;
+          while (true) {
+            const bool have = j < left;
+            const uint32_t g = gs + static_cast<uint32_t>(j);
+            if (have) {
+              const uint32_t ks = g % KS;
+              if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, status, abort_flag))) break;
+              tc_fence_after();
+              if (leader) {
+                const uint64_t a0 = dK + ks * kTileStep;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                  mma_ss(tS + (k & 1u) * kOwnCols, a0 + (c >> 2) * (1024 >> 4) + (c & 3) * 2,
+                         dQs + (c >> 2) * (L::kChunkBytes >> 4) + (c & 3) * 2, idesc_s, c != 0 ? 1u : 0u);
+                mma_commit(BAR_SO(t, k));
+                mma_commit(BAR_KE(ks));
+                mbar_arrive(BAR_KE(ks));
               }
-              mma_commit(BAR_SF(t));
-              mma_commit(BAR_KE(ks));
-              mbar_arrive(BAR_KE(ks));
+              __syncwarp();
             }
-            __syncwarp();
-            if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, status, abort_flag))) break;
-            if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, status, abort_flag))) break;
-            if (!(ok = wait_all(BAR_PR(t), steps_t & 1u, status, abort_flag))) break;
-            tc_fence_after();
-            if (leader) {
-              const uint64_t a0 = dVt + vs * kTileStep;
-#pragma unroll 1
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
-                mma_ss(tO, a0 + static_cast<uint64_t>(off >> 4), dP + (kk >> 2) * (kOwnCols * 128 >> 4) + (kk & 3) * 2,
-                       idesc_o, (j > first || kk > 0) ? 1u : 0u);
+            if (k > 0) {   // the product of the step before
+              const uint32_t vs = pg % VS;
+              if (!(ok = wait_all(BAR_VF(vs), (pg / VS) & 1u, status, abort_flag))) break;
+              if (pfirst && pused > 0 && !(ok = wait_all(BAR_OF(t), (pused - 1) & 1u, status, abort_flag))) break;
+              if (!(ok = wait_all(BAR_PR(t), steps_t & 1u, status, abort_flag))) break;
+              ++steps_t;
+              tc_fence_after();
+              if (leader) {
+                const uint64_t a0 = dVt + vs * kTileStep, b0 = dP + ((k & 1u) ^ 1u) * (kOwnPBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                  const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
+                  mma_ss(tO, a0 + static_cast<uint64_t>(off >> 4), b0 + (kk >> 2) * (kOwnCols * 128 >> 4) + (kk & 3) * 2,
+                         idesc_o, (!pfirst || kk > 0) ? 1u : 0u);
+                }
+                mma_commit(BAR_OD(t));
+                mma_commit(BAR_VE(vs));
+                mbar_arrive(BAR_VE(vs));
               }
-              if (j + stride >= tiles) mma_commit(BAR_OD(t));
-              mma_commit(BAR_VE(vs));
-              mbar_arrive(BAR_VE(vs));
+              __syncwarp();
             }
-            __syncwarp();
+            if (!have) break;
+            pg = g;
+            pfirst = sfirst;
+            pused = used;
+            sfirst = false;
+            ++k;
+            j += 2;
+            while (j >= left) {   // the next segment with steps of this row tile
+              ++n;
+              const uint32_t en = n % kSegments;
+              if (!(ok = wait_all(BAR_GF(en), (n / kSegments) & 1u, status, abort_flag))) break;
+              gs = __shfl_sync(0xffffffffu, ring[en].g0, 0);
+              left = __shfl_sync(0xffffffffu, ring[en].tiles, 0);
+              j = (t ^ __shfl_sync(0xffffffffu, ring[en].tile_first, 0)) & 1;
+              dQs = dQ + static_cast<uint64_t>(__shfl_sync(0xffffffffu, ring[en].qslot, 0) * 64);
+              __syncwarp();
+              if (leader) mbar_arrive(BAR_GE(en));
+              if (left == 0) break;
+              if (j < left) {
+                ++used;
+                sfirst = true;
+                ok = wait_all(BAR_QF(t, used), (used / kQLoads) & 1u, status, abort_flag);
+              }
+            }
+            if (!ok) break;
           }
-          ++used;
-          continue;
+          break;   // prefixes come first: no segment is left
         }
+        if (wide && t == 1 && !(ok = wait_all(BAR_ST, wides++ & 1u, status, abort_flag))) break;
         for (int j = first; j < tiles; j += stride, ++steps_t) {
           const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
           // S_t = Q_t K^T, 16 columns of d a step.  (The issue loops are rolled: a turn
@@ -794,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + (t == 0 ? L::kTmO0 : L::kTmO1) + lane_off;
     const float c2 = a.scale_log2;
     bool ok = true;
-    uint32_t steps_t = 0, held = 0, exchanges = 0;   // S/P and O barrier phases of this row tile
+    uint32_t steps_t = 0, held = 0, exchanges = 0, own_k = 0;   // S/P and O barrier phases of this row tile; own-keys steps
     for (uint32_t seg = 0; ok; ++seg) {
       const uint32_t e = seg % kSegments;
       ok = wait_all(BAR_GF(e), (seg / kSegments) & 1u, status, abort_flag);
@@ -822,8 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < L::kChunks; ++c)
 #pragma unroll
-            for (int z = 0; z < 8; ++z)
-              reinterpret_cast<uint4*>(base + c * a.page_size * 128)[z] = make_uint4(0u, 0u, 0u, 0u);
+            for (int z = 0; z < 8; ++z)   // eight rows' pieces of eight different banks at a time
+              reinterpret_cast<uint4*>(base + c * a.page_size * 128)[(z + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
         }
         return true;
       };
@@ -862,52 +903,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        uint8_t* prow = smem + L::kQ + t * L::kTileBytes + kOwnP + (lane_row >> 6) * (kOwnCols * 128);
-        for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t) {
-          ok = wait_all(BAR_SF(t), steps_t & 1u, status, abort_flag);
+        uint8_t* const prow = smem + L::kQ + t * L::kTileBytes + kOwnP + (lane_row >> 6) * (kOwnCols * 128);
+        const uint32_t pcol = static_cast<uint32_t>(((lane_row & 63) >> 3) * 16), pbyte = static_cast<uint32_t>((lane_row & 7) * 2);
+        for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t, ++own_k) {
+          ok = wait_all(BAR_SO(t, own_k), (own_k >> 1) & 1u, status, abort_flag);
           if (!ok) break;
           tc_fence_after();
+          uint32_t sr[kG];
+          tmem_ld8(tS + (own_k & 1u) * kOwnCols, sr);
           const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
           const bool is_key = lane_row >= lo && lane_row < lim;
           if ((lim < kTile || lo > 0) && !(ok = zero_values(j, lo, lim))) break;
-          uint32_t sr[kG];
-          tmem_ld8(tS, sr);
           tmem_wait_ld();
           float s[kG], mx[kG];
+          bool raise = false;   // some row's max moves (by more than the margin)
 #pragma unroll
           for (int i = 0; i < kG; ++i) {
             s[i] = is_key ? __uint_as_float(sr[i]) : -INFINITY;
             mx[i] = warp_max(s[i]);
           }
           if (!(ok = exchange(mx, [](float x, float y) { return fmaxf(x, y); }))) break;
-          float alpha[kG];
-          bool rescale = false;
 #pragma unroll
-          for (int i = 0; i < kG; ++i) {
-            const float m_new = fmaxf(m[i], mx[i]);
-            const bool upd = (m[i] == -INFINITY) || ((m_new - m[i]) * c2 > kRescaleLog2);
-            alpha[i] = (upd && m[i] != -INFINITY) ? ex2((m[i] - m_new) * c2) : 1.f;
-            if (upd) m[i] = m_new;
-            rescale = rescale || (i < G && alpha[i] != 1.f);
-          }
-          if (!first && rescale) {   // all 128 threads alike
-            uint32_t orr[kG];
-            tmem_ld8(tO, orr);
-            tmem_wait_ld();
+          for (int i = 0; i < kG; ++i) raise = raise || (i < G && (mx[i] - m[i]) * c2 > kRescaleLog2);
+          if (raise) {   // all 128 threads alike
+            float alpha[kG];
 #pragma unroll
-            for (int i = 0; i < kG; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha[i]);
-            tmem_st8(tO, orr);
-            tmem_wait_st();
+            for (int i = 0; i < kG; ++i) {
+              const float m_new = fmaxf(m[i], mx[i]);
+              alpha[i] = m[i] == m_new ? 1.f : ex2((m[i] - m_new) * c2);   // 0 from -inf
+              m[i] = m_new;
+              l[i] *= alpha[i];
+            }
+            if (!first) {   // O holds the products of the steps before, once the last of them is done
+              if (!(ok = wait_all(BAR_OD(t), (held - 1) & 1u, status, abort_flag))) break;
+              tc_fence_after();
+              uint32_t orr[kG];
+              tmem_ld8(tO, orr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < kG; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha[i]);
+              tmem_st8(tO, orr);
+              tmem_wait_st();
+            }
           }
+          ++held;   // this step's product is one phase of o_done
           // weights into P^T [query][key], 128-byte rows of 64 keys, 16-byte pieces swizzled by the row
-#pragma unroll
-          for (int i = 0; i < kG; ++i) {
+          uint8_t* const pk = prow + (own_k & 1u) * kOwnPBytes + pbyte;
+          auto weigh = [&](int i) {
             const float negm = (m[i] == -INFINITY) ? 0.f : -m[i] * c2;
             const float p = ex2(fmaf(s[i], c2, negm));
-            l[i] = fmaf(l[i], alpha[i], p);
-            if (i < G)
-              *reinterpret_cast<__nv_bfloat16*>(prow + i * 128 + ((((lane_row & 63) >> 3) ^ i) << 4) + (lane_row & 7) * 2) =
-                  __float2bfloat16(p);
+            l[i] += p;
+            *reinterpret_cast<__nv_bfloat16*>(pk + i * 128 + (pcol ^ (i * 16))) = __float2bfloat16(p);
+          };
+          weigh(0);
+          if (G > 1) weigh(1);
+          if (G > 2) {
+            weigh(2);
+            weigh(3);
+          }
+          if (G > 4) {
+#pragma unroll
+            for (int i = 4; i < kG; ++i) weigh(i);
           }
           fence_proxy_async_smem();   // P (and zeroed V) before the products read them
           tc_fence_before();
@@ -917,12 +973,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the partial: this thread has column `lane_row` of d
 #pragma unroll
         for (int i = 0; i < kG; ++i)
+          if (i < G) {
 #pragma unroll
-          for (int x = 16; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-        ok = exchange(l, [](float x, float y) { return x + y; }) && wait_all(BAR_OD(t), held & 1u, status, abort_flag);
+            for (int x = 16; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+          }
+        ok = exchange(l, [](float x, float y) { return x + y; }) && wait_all(BAR_OD(t), (held - 1) & 1u, status, abort_flag);
         tc_fence_after();
         if (!ok) break;
-        ++held;
         uint32_t orr[kG];
         tmem_ld8(tO, orr);
         tmem_wait_ld();
@@ -1031,6 +1088,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(c0 < 64 ? BAR_PH(t) : BAR_PR(t));
+            // row tile 1 starts a wide segment when tile 0 is here in its first step, so that one tile's products run under
+            // the other's softmax; started together they stay together (5000 cycles a step instead of XX)
+            if (c0 < 64 && first && sg.wide && t == 0 && lane == 0) mbar_arrive(BAR_ST);
           }
         }
       }
@@ -1082,12 +1142,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Combine: one CTA per (KV head, sequence).  Thread (p, c4, g) joins every NP-th
-// partial of columns [4 c4, 4 c4 + 4) of query head g, the NP runs meet in
-// shared memory.  Weights e^(lse_i - max) over all partials of a row.
+// Combine: one CTA per (KV head, sequence), thread (c4, g) joins the partials of
+// columns [4 c4, 4 c4 + 4) of query head g.  Weights e^(lse_i - max) over all
+// partials of a row.  No shared memory and few registers, so its first CTAs wait
+// on the SMs beside the attend kernel's.
 // ---------------------------------------------------------------------------
-constexpr int kCombineThreads = 512;
-
 __device__ __forceinline__ long long divide(long long x, long long y) {   // both >= 0; in 32 bits where it fits
   return ((x | y) >> 32) == 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(y) : x / y;
 }
@@ -1098,14 +1157,8 @@ __device__ __forceinline__ void unit_ctas(long long x0, int tiles, int shift, lo
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const SharedArgs a, __nv_bfloat16* o,
-                                                                       float* lse) {
-  constexpr int kPer = G * D / 4, NP = kCombineThreads / kPer;
-  static_assert(kPer <= kCombineThreads && kCombineThreads % kPer == 0, "threads per partial");
-  __shared__ float s_m[kCombineThreads], s_l[kCombineThreads];
-  __shared__ float4 s_o[kCombineThreads];
-  const int hkv = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
-  const int p0 = tid / kPer, c4 = (tid % kPer) / G, gq = tid % G;
+__global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedArgs a, __nv_bfloat16* o, float* lse) {
+  const int hkv = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, c4 = tid / G, gq = tid % G;
   grid_wait();   // the partials are complete
   const SeqPlan sp = a.seqs[seq];
   const long long per = *a.per_cta;
@@ -1143,18 +1196,18 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
   };
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 4;   // partials loaded before the first is joined
-  for (int i0 = p0; i0 < n; i0 += kAhead * NP) {
+  constexpr int kAhead = 6;   // partials loaded before the first is joined
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
     float w[kAhead];
     float4 v[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       w[k] = -INFINITY;
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + k * NP < n) {
+      if (i0 + k < n) {
         const float* pw;
         const float4* pv;
-        place(i0 + k * NP, pw, pv);
+        place(i0 + k, pw, pv);
         w[k] = *pw;
         v[k] = *pv;
       }
@@ -1178,39 +1231,18 @@ __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const S
         acc.w = fmaf(s1, v[k].w, acc.w);
       }
   }
-  s_m[tid] = m;
-  s_l[tid] = l;
-  s_o[tid] = acc;
-  __syncthreads();
-  if (hkv == 0 && seq == 0 && tid < 32) {   // the call's status: any CTA's
+  if (hkv == 0 && seq == 0 && tid == 0) {   // the call's status: any CTA's
     unsigned bits = 0;
-    for (int c = tid; c < a.n_ctas; c += 32) bits |= a.cta_status[c];
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    if (tid == 0) *a.status = bits;
+    for (int c = 0; c < a.n_ctas; ++c) bits |= a.cta_status[c];
+    *a.status = bits;
   }
-  if (p0 != 0) return;
-  float M = m;
-  for (int p = 1; p < NP; ++p) M = fmaxf(M, s_m[p * kPer + tid]);
-  float tot = 0.f;
-  float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < NP; ++p) {
-    const int e = p * kPer + tid;
-    if (s_m[e] == -INFINITY) continue;
-    const float w = __expf(s_m[e] - M);
-    const float4 v = s_o[e];
-    tot = fmaf(w, s_l[e], tot);
-    out.x = fmaf(w, v.x, out.x);
-    out.y = fmaf(w, v.y, out.y);
-    out.z = fmaf(w, v.z, out.z);
-    out.w = fmaf(w, v.w, out.w);
-  }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
   const size_t orow = static_cast<size_t>(seq) * a.Hq + hkv * G + gq;
   uint2 w2;
-  w2.x = pack_bf16x2(out.x * inv, out.y * inv);
-  w2.y = pack_bf16x2(out.z * inv, out.w * inv);
+  w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(o + orow * D)[c4] = w2;
-  if (c4 == 0 && lse) lse[orow] = tot > 0.f ? M + __logf(tot) : -INFINITY;
+  if (c4 == 0 && lse) lse[orow] = l > 0.f ? m + __logf(l) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -1274,10 +1306,10 @@ template <int D>
 cudaError_t launch_combine(const SharedArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.num_seqs));
   switch (a.G) {
-    case 1: return launch(shared_combine_kernel<D, 1>, grid, kCombineThreads, 0, true, stream, a, o, lse);
-    case 2: return launch(shared_combine_kernel<D, 2>, grid, kCombineThreads, 0, true, stream, a, o, lse);
-    case 4: return launch(shared_combine_kernel<D, 4>, grid, kCombineThreads, 0, true, stream, a, o, lse);
-    default: return launch(shared_combine_kernel<D, 8>, grid, kCombineThreads, 0, true, stream, a, o, lse);
+    case 1: return launch(shared_combine_kernel<D, 1>, grid, 1 * D / 4, 0, true, stream, a, o, lse);
+    case 2: return launch(shared_combine_kernel<D, 2>, grid, 2 * D / 4, 0, true, stream, a, o, lse);
+    case 4: return launch(shared_combine_kernel<D, 4>, grid, 4 * D / 4, 0, true, stream, a, o, lse);
+    default: return launch(shared_combine_kernel<D, 8>, grid, 8 * D / 4, 0, true, stream, a, o, lse);
   }
 }
 
