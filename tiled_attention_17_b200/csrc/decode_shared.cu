@@ -65,6 +65,8 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, unsigned
   return __all_sync(0xffffffffu, ok);   // one answer for the warp
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Eight 32-bit columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -181,6 +183,8 @@ __device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int 
   const int lane = threadIdx.x & 31, i = w * 32 + lane;
   Window r;
   r.it = describe_item(a, groups, i, bad);
+  if (r.it.end > r.it.base)   // its first pages' table entries, soon wanted by the CTA that starts there
+    prefetch_l2(a.block_table + static_cast<size_t>(r.it.first) * a.max_pages + r.it.base / a.page_size);
   const int tiles = tiles_of(r.it.end - r.it.base);
   const int units = tiles > 0 ? blocks_of(r.it.n, a.G) * a.Hkv : 0, own_units = i < groups ? units : 0;
   r.cost = (static_cast<long long>(units) * tiles) << shift_of(r.it.n, a.G);
@@ -309,6 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   grid_launch_dependents();   // the combine kernel waits for this grid before it reads anything
+  // the plan's inputs on their way into L2 while barriers and tensor memory are set up (32 numbers a line)
+  for (int i = threadIdx.x * 32; i < a.num_seqs; i += kThreads * 32) prefetch_l2(a.seq_lens + i);
+  for (int i = threadIdx.x * 32; i < a.num_groups; i += kThreads * 32) {
+    prefetch_l2(a.group_offsets + i);
+    prefetch_l2(a.prefix_lens + i);
+  }
   // ---- setup
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < KS; ++s) {
@@ -1196,7 +1206,7 @@ __global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedA
   };
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 6;   // partials loaded before the first is joined
+  constexpr int kAhead = 8;   // partials loaded before the first is joined
   for (int i0 = 0; i0 < n; i0 += kAhead) {
     float w[kAhead];
     float4 v[kAhead];
@@ -1231,10 +1241,12 @@ __global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedA
         acc.w = fmaf(s1, v[k].w, acc.w);
       }
   }
-  if (hkv == 0 && seq == 0 && tid == 0) {   // the call's status: any CTA's
+  constexpr int kGather = G * D / 4 < 32 ? G * D / 4 : 32;
+  if (hkv == 0 && seq == 0 && tid < kGather) {   // the call's status: any CTA's
     unsigned bits = 0;
-    for (int c = 0; c < a.n_ctas; ++c) bits |= a.cta_status[c];
-    *a.status = bits;
+    for (int c = tid; c < a.n_ctas; c += kGather) bits |= a.cta_status[c];
+    bits = __reduce_or_sync(kGather == 32 ? 0xffffffffu : (1u << kGather) - 1u, bits);
+    if (tid == 0) *a.status = bits;
   }
   const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
   const size_t orow = static_cast<size_t>(seq) * a.Hq + hkv * G + gq;
