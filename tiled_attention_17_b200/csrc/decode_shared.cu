@@ -266,9 +266,9 @@ struct AttendLayout {
   static constexpr int kSeg = kV + kVStages * kTileBytes;
   static constexpr int kRed = kSeg + kSegments * static_cast<int>(sizeof(Segment));   // [row tile][2][4 warps][8] floats
   static constexpr int kBar = kRed + 2 * 2 * 4 * 8 * 4;
-  // k_full, k_empty, v_full, v_empty; per row tile: s_full, p_half, p_ready, o_free, o_done, exchange, own s_full[2], q_full[]; segment full, empty;
-  // mma_done, windows read, staggered start
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 16 + 2 * kQLoads + 2 * kSegments + 3;
+  // k_full, k_empty, v_full, v_empty; per row tile: s_full[2], p_ready[2], o_free, o_done, exchange, own s_full[2], q_full[]; segment full, empty;
+  // mma_done, windows read
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 18 + 2 * kQLoads + 2 * kSegments + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag, status word; line's cost, CTA's share
   // slack to align the base to 1024 B; with d = 64 the own-keys product reads 64 rows it does not need, 1 KB on
   static constexpr int kAlloc = kMisc + 32 + 1024 + (D == 64 ? 1024 : 0);
@@ -289,22 +289,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
   constexpr uint32_t KS = L::kKStages, VS = L::kVStages;
-  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (16 + 2 * kQLoads);
+  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (18 + 2 * kQLoads);
   auto BAR_KF = [&](uint32_t s) { return bar0 + 8u * s; };
   auto BAR_KE = [&](uint32_t s) { return bar0 + 8u * (KS + s); };
   auto BAR_VF = [&](uint32_t s) { return bar0 + 8u * (2 * KS + s); };
   auto BAR_VE = [&](uint32_t s) { return bar0 + 8u * (2 * KS + VS + s); };
-  auto BAR_SF = [&](int t) { return bar_t + 8u * t; };
-  auto BAR_PH = [&](int t) { return bar_t + 8u * (2 + t); };
-  auto BAR_PR = [&](int t) { return bar_t + 8u * (4 + t); };
-  auto BAR_OF = [&](int t) { return bar_t + 8u * (6 + t); };
-  auto BAR_OD = [&](int t) { return bar_t + 8u * (8 + t); };
-  auto BAR_X = [&](int t) { return bar_t + 8u * (10 + t); };
-  auto BAR_SO = [&](int t, uint32_t k) { return bar_t + 8u * (12 + 2 * t + (k & 1u)); };
-  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (16 + t * kQLoads + load % kQLoads); };
+  auto BAR_SF = [&](int t, int h) { return bar_t + 8u * (2 * t + h); };
+  auto BAR_PR = [&](int t, int h) { return bar_t + 8u * (4 + 2 * t + h); };
+  auto BAR_OF = [&](int t) { return bar_t + 8u * (8 + t); };
+  auto BAR_OD = [&](int t) { return bar_t + 8u * (10 + t); };
+  auto BAR_X = [&](int t) { return bar_t + 8u * (12 + t); };
+  auto BAR_SO = [&](int t, uint32_t k) { return bar_t + 8u * (14 + 2 * t + (k & 1u)); };
+  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (18 + t * kQLoads + load % kQLoads); };
   auto BAR_GF = [&](uint32_t e) { return bar_s + 8u * e; };
   auto BAR_GE = [&](uint32_t e) { return bar_s + 8u * (kSegments + e); };
-  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments, BAR_GO = BAR_FIN + 8u, BAR_ST = BAR_FIN + 16u;
+  const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments, BAR_GO = BAR_FIN + 8u;
   Segment* ring = reinterpret_cast<Segment*>(smem + L::kSeg);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -331,9 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       for (uint32_t u = 0; u < kQLoads; ++u) mbar_init(BAR_QF(t, u), 1);
-      mbar_init(BAR_SF(t), 1);
-      mbar_init(BAR_PH(t), 128);
-      mbar_init(BAR_PR(t), 128);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(BAR_SF(t, h), 1);
+        mbar_init(BAR_PR(t, h), 128);
+      }
       mbar_init(BAR_OF(t), 128);
       mbar_init(BAR_OD(t), 1);
       mbar_init(BAR_X(t), 4);   // one lane of each softmax warp
@@ -346,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(BAR_FIN, 2);
     mbar_init(BAR_GO, 1);
-    mbar_init(BAR_ST, 4);   // one lane of each softmax warp of row tile 0
     *abort_flag = 0;
     *status = 0;
     fence_mbar_init();
@@ -668,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // two tiles' chains add up (a narrow step took 2.4 us), from two they overlap.
       const int t = warp == kMmaWarp1 ? 1 : 0;
       const bool leader = elect_one_sync();
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile, false);
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile / 2, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kTile, D, true);
       const uint32_t tS = tmem + (t ? L::kTmS1 : L::kTmS0), tO = tmem + (t ? L::kTmO1 : L::kTmO0);
       constexpr bool kTwo = L::kChunks == 2;
@@ -681,8 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // page-major V: 16-key step kk starts at byte 2048 (kk + (kk & vmask))
       const int vmask = ~(max(ps / 16, 1) - 1);
       bool ok = true;
-      uint32_t wides = 0;
-      uint32_t steps_t = 0, used = 0;   // steps and segments of this row tile: S/P and Q/O barrier phases
+      // steps and segments of this row tile, and products with V taken: S/P, Q/O and o_done barrier phases
+      uint32_t steps_t = 0, used = 0, products = 0;
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
         if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, status, abort_flag))) break;
@@ -738,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t vs = pg % VS;
               if (!(ok = wait_all(BAR_VF(vs), (pg / VS) & 1u, status, abort_flag))) break;
               if (pfirst && pused > 0 && !(ok = wait_all(BAR_OF(t), (pused - 1) & 1u, status, abort_flag))) break;
-              if (!(ok = wait_all(BAR_PR(t), steps_t & 1u, status, abort_flag))) break;
+              if (!(ok = wait_all(BAR_PR(t, 0), steps_t & 1u, status, abort_flag))) break;
               ++steps_t;
               tc_fence_after();
               if (leader) {
@@ -783,52 +782,78 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           break;   // prefixes come first: no segment is left
         }
-        if (wide && t == 1 && !(ok = wait_all(BAR_ST, wides++ & 1u, status, abort_flag))) break;
-        for (int j = first; j < tiles; j += stride, ++steps_t) {
-          const uint32_t g = g0 + static_cast<uint32_t>(j), ks = g % KS, vs = g % VS;
-          // S_t = Q_t K^T, 16 columns of d a step.  (The issue loops are rolled: a turn
-          // takes about the 64 cycles of its MMA, and the code stays small.)
-          if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, status, abort_flag))) break;
-          tc_fence_after();
+        // A step goes in two halves of 64 keys, each with its own scores and weights
+        // in tensor memory: the scores of one half are formed while the softmax is at
+        // the other, and the next step's as soon as the product that reads the weights
+        // in their place is complete.  (Complete, not issued: products into different
+        // accumulators are not ordered.)
+        auto scores = [&](uint32_t g, int h) {   // S_t[h] = Q_t K[64 h ..]^T
           if (leader) {
-            uint64_t a0 = dQ, b0 = dK + ks * kTileStep;
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              mma_ss(tS, a0, b0, idesc_qk, k != 0 ? 1u : 0u);
-              a0 += (k & 3) == 3 ? (L::kChunkBytes >> 4) - 6 : 2;   // within a 128-byte chunk, then the next one
-              b0 += (k & 3) == 3 ? (1024 >> 4) - 6 : 2;
+            const uint64_t b0 = dK + (g % KS) * kTileStep + static_cast<uint64_t>(h) * (L::kChunks * 512);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              mma_ss(tS + h * 64, dQ + (c >> 2) * (L::kChunkBytes >> 4) + (c & 3) * 2,
+                     b0 + (c >> 2) * (1024 >> 4) + (c & 3) * 2, idesc_qk, c != 0 ? 1u : 0u);
+            mma_commit(BAR_SF(t, h));
+            if (h == 1) {
+              mma_commit(BAR_KE(g % KS));   // K's release also frees the query tile after a segment's last step
+              if (!wide) mbar_arrive(BAR_KE(g % KS));
             }
-            mma_commit(BAR_SF(t));
-            mma_commit(BAR_KE(ks));   // K's release also frees the query tile after a segment's last step
-            if (!wide) mbar_arrive(BAR_KE(ks));
           }
           __syncwarp();
-          // O_t += P_t V, 64 keys as soon as their weights are written.  The first of a
-          // segment overwrites O_t: the epilogue before must have read it.
-          if (!(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, status, abort_flag))) break;
+        };
+        uint32_t gs = g0 + static_cast<uint32_t>(first);   // ring position of the next scores
+        int q = 0;                                         // halves of them formed
+        int j = first - stride;                            // step of the products
+        while (true) {
+          const bool more = j + stride < tiles;
+          const uint32_t g = gs - static_cast<uint32_t>(stride), vs = g % VS;
+          q = 0;
+          if (j >= 0 && !(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, status, abort_flag))) break;
+          // the first product of a segment overwrites O_t: the epilogue before must have read it
           if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, status, abort_flag))) break;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {   // BAR_PH(t), then BAR_PR(t)
-            if (!(ok = wait_all(BAR_PH(t) + 16u * half, steps_t & 1u, status, abort_flag))) break;
-            tc_fence_after();
-            if (leader) {
-              const uint64_t b0 = dV + vs * kTileStep;
-#pragma unroll 1
-              for (int kk = half * 4; kk < half * 4 + 4; ++kk) {
-                const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
-                mma_ts(tO, tS + kk * 8, b0 + static_cast<uint64_t>(off >> 4), idesc_pv, (j > first || kk > 0) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            if (j >= 0) {   // O_t += P_t[h] V[64 h ..]
+              if (!(ok = wait_all(BAR_PR(t, h), steps_t & 1u, status, abort_flag))) break;
+              tc_fence_after();
+              if (leader) {
+                const uint64_t b0 = dV + vs * kTileStep;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const int kk = h * 4 + c;
+                  const uint32_t off = kTwo ? static_cast<uint32_t>((kk + (kk & vmask)) << 11) : kk * 2048u;
+                  mma_ts(tO, tS + h * 64 + c * 8, b0 + static_cast<uint64_t>(off >> 4), idesc_pv,
+                         (j > first || kk > 0) ? 1u : 0u);
+                }
+                mma_commit(BAR_OD(t));
               }
+              __syncwarp();
+              if (!(ok = wait_all(BAR_OD(t), products++ & 1u, status, abort_flag))) break;
             }
-            __syncwarp();
+            // the next step's scores: of this half if K is there, else both later
+            const uint32_t kf = BAR_KF(gs % KS), kph = (gs / KS) & 1u;
+            if (more && (h == 1 || __all_sync(0xffffffffu, mbar_try_wait(kf, kph)))) {
+              if (!(ok = wait_all(kf, kph, status, abort_flag))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (; q <= h; ++q) scores(gs, q);
+            }
           }
           if (!ok) break;
-          if (leader) {
-            if (j + stride >= tiles) mma_commit(BAR_OD(t));   // the segment's O is complete
-            mma_commit(BAR_VE(vs));
-            if (!wide) mbar_arrive(BAR_VE(vs));
+          if (j >= 0) {
+            if (leader) {
+              mma_commit(BAR_VE(vs));
+              if (!wide) mbar_arrive(BAR_VE(vs));
+            }
+            __syncwarp();
+            ++steps_t;
           }
-          __syncwarp();
+          if (!more) break;
+          j += stride;
+          gs += static_cast<uint32_t>(stride);
         }
+        if (!ok) break;
         ++used;
       }
       // no commit may still be pending when the CTA exits
@@ -845,7 +870,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + (t == 0 ? L::kTmO0 : L::kTmO1) + lane_off;
     const float c2 = a.scale_log2;
     bool ok = true;
-    uint32_t steps_t = 0, held = 0, exchanges = 0, own_k = 0;   // S/P and O barrier phases of this row tile; own-keys steps
+    uint32_t steps_t = 0, held = 0, exchanges = 0, own_k = 0;   // S/P and o_done phases of this row tile; own-keys steps
+    // Waits for the last product with V this row tile's weights went into.  Every
+    // one is waited for, and before the weights of the next are handed over: a
+    // barrier tells only the parity of its phase, so none may be skipped.
+    bool due = false;
+    auto product_done = [&]() {
+      if (!due) return true;
+      due = false;
+      const bool done = wait_all(BAR_OD(t), held++ & 1u, status, abort_flag);
+      tc_fence_after();
+      return done;
+    };
     for (uint32_t seg = 0; ok; ++seg) {
       const uint32_t e = seg % kSegments;
       ok = wait_all(BAR_GF(e), (seg / kSegments) & 1u, status, abort_flag);
@@ -945,8 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               l[i] *= alpha[i];
             }
             if (!first) {   // O holds the products of the steps before, once the last of them is done
-              if (!(ok = wait_all(BAR_OD(t), (held - 1) & 1u, status, abort_flag))) break;
-              tc_fence_after();
+              if (!(ok = product_done())) break;
               uint32_t orr[kG];
               tmem_ld8(tO, orr);
               tmem_wait_ld();
@@ -956,7 +991,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_st();
             }
           }
-          ++held;   // this step's product is one phase of o_done
           // weights into P^T [query][key], 128-byte rows of 64 keys, 16-byte pieces swizzled by the row
           uint8_t* const pk = prow + (own_k & 1u) * kOwnPBytes + pbyte;
           auto weigh = [&](int i) {
@@ -976,8 +1010,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 4; i < kG; ++i) weigh(i);
           }
           fence_proxy_async_smem();   // P (and zeroed V) before the products read them
+          if (!(ok = product_done())) break;
           tc_fence_before();
-          mbar_arrive(BAR_PR(t));
+          mbar_arrive(BAR_PR(t, 0));
+          due = true;
         }
         if (!ok) break;
         // ---- the partial: this thread has column `lane_row` of d
@@ -987,9 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 16; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
           }
-        ok = exchange(l, [](float x, float y) { return x + y; }) && wait_all(BAR_OD(t), (held - 1) & 1u, status, abort_flag);
-        tc_fence_after();
-        if (!ok) break;
+        if (!(ok = exchange(l, [](float x, float y) { return x + y; }) && product_done())) break;
         uint32_t orr[kG];
         tmem_ld8(tO, orr);
         tmem_wait_ld();
@@ -1008,84 +1042,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       float m = -INFINITY, l = 0.f;
-      for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t) {
-        ok = wait_all(BAR_SF(t), steps_t & 1u, status, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
+      for (bool first = true; j < sg.tiles && ok; j += stride, ++steps_t) {
         // keys of this tile: columns [lo, lim); the rest of its shared memory holds none that count
         const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
         const bool need_mask = lim < kTile || lo > 0;
-        if (need_mask) {
-          if (!(ok = zero_values(j, lo, lim))) break;
-          fence_proxy_async_smem();
-        }
-        if (!warp_live) {   // no row of this warp counts: its P may hold anything
-          mbar_arrive(BAR_PH(t));
-          mbar_arrive(BAR_PR(t));
-          continue;
-        }
-        // Two passes over the scores in TMEM, 32 columns at a time: the row max,
-        // then the weights.  Loading them twice costs less than holding all 128
-        // in registers with the code unrolled over them: that code did not fit the
-        // instruction cache beside the other roles (see the top of the file).
-        auto load = [&](int c0, uint32_t (&r)[32]) {
-          tmem_ld32(tS + c0, r);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h, first = false) {   // 64 keys
+          ok = wait_all(BAR_SF(t, h), steps_t & 1u, status, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (need_mask && h == 0) {
+            if (!(ok = zero_values(j, lo, lim))) break;
+            fence_proxy_async_smem();
+          }
+          if (!warp_live) {   // no row of this warp counts: its P may hold anything
+            if (!(ok = product_done())) break;
+            mbar_arrive(BAR_PR(t, h));
+            due = true;
+            continue;
+          }
+          uint32_t sr[2][32];
+          tmem_ld32(tS + h * 64, sr[0]);
+          tmem_ld32(tS + h * 64 + 32, sr[1]);
           tmem_wait_ld();
           if (need_mask) {
-            // bit c: column c0 + c is a key
-            const int a0 = max(lo - c0, 0), b0 = min(max(lim - c0, 0), 32);
-            const uint32_t keys = b0 > a0 ? (0xffffffffu >> (32 - b0)) & (0xffffffffu << a0) : 0u;
+            const unsigned c0 = static_cast<unsigned>(h * 64 - lo), span = static_cast<unsigned>(lim - lo);
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(keys >> c & 1u)) r[c] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 64; ++c)
+              if (c0 + c >= span) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           }
-        };
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c0 = 0; c0 < kTile; c0 += 32) {
-          uint32_t sr[32];
-          load(c0, sr);
-          const float* s = reinterpret_cast<const float*>(sr);
-          float r0 = -INFINITY, r1 = -INFINITY;
+          const float* s = reinterpret_cast<const float*>(&sr[0][0]);
+          float mx;
+          {
+            float r0 = -INFINITY, r1 = -INFINITY, r2 = -INFINITY, r3 = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            r0 = fmax3(r0, s[c + 0], s[c + 1]);
-            r1 = fmax3(r1, s[c + 2], s[c + 3]);
+            for (int c = 0; c < 64; c += 8) {
+              r0 = fmax3(r0, s[c + 0], s[c + 1]);
+              r1 = fmax3(r1, s[c + 2], s[c + 3]);
+              r2 = fmax3(r2, s[c + 4], s[c + 5]);
+              r3 = fmax3(r3, s[c + 6], s[c + 7]);
+            }
+            mx = fmaxf(fmax3(r0, r1, r2), r3);
           }
-          mx = fmax3(mx, r0, r1);
-        }
-        const float m_new = fmaxf(m, mx);
-        const bool upd = (m == -INFINITY) || ((m_new - m) * c2 > kRescaleLog2);
-        const float m_use = upd ? m_new : m;
-        const float alpha = (upd && m != -INFINITY) ? ex2((m - m_use) * c2) : (m == -INFINITY ? 0.f : 1.f);
-        const float negm = (m_use == -INFINITY) ? 0.f : -m_use * c2;
-        m = m_use;
-        // rows that do not count hold anything: they ask for no rescale
-        if (!first && __any_sync(0xffffffffu, live && alpha != 1.f)) {
+          // rows that do not count hold anything: they ask for no rescale
+          if (__any_sync(0xffffffffu, live && (mx - m) * c2 > kRescaleLog2)) {
+            const float m_new = fmaxf(m, mx);
+            const float alpha = m == m_new ? 1.f : ex2((m - m_new) * c2);   // 0 from -inf
+            m = m_new;
+            l *= alpha;
+            if (!first) {   // O holds the products of the halves before, once the last of them is done
+              if (!(ok = product_done())) break;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t orr[32];
-            tmem_ld32(tO + c * 32, orr);
-            tmem_wait_ld();
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t orr[32];
+                tmem_ld32(tO + c * 32, orr);
+                tmem_wait_ld();
 #pragma unroll
-            for (int z = 0; z < 32; ++z) orr[z] = __float_as_uint(__uint_as_float(orr[z]) * alpha);
-            tmem_st32(tO + c * 32, orr);
+                for (int z = 0; z < 32; ++z) orr[z] = __float_as_uint(__uint_as_float(orr[z]) * alpha);
+                tmem_st32(tO + c * 32, orr);
+              }
+            }
           }
-        }
-        l *= alpha;
-        // Weights 2^((s - m) c2), packed to bf16 for the tensor product (the rounding
-        // of the prefill kernels; the sum is of the unrounded values).  c2 > 0 (see
-        // the host side), so masked columns are exactly 0.  The weights take the columns
-        // of scores already read.
-#pragma unroll 1
-        for (int c0 = 0; c0 < kTile; c0 += 32) {
-          uint32_t sr[32], pk[16];
-          load(c0, sr);
-          const float* s = reinterpret_cast<const float*>(sr);
+          // Weights 2^((s - m) c2), packed to bf16 for the tensor product (the rounding
+          // of the prefill kernels; the sum is of the unrounded values).  c2 > 0 (see
+          // the host side), so masked columns are exactly 0.  The weights take the
+          // columns of their scores.
+          const float negm = (m == -INFINITY) ? 0.f : -m * c2;
           const float2 c2v = make_float2(c2, c2), negv = make_float2(negm, negm);
           float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
+          uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 32; ++i) {
             const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), c2v, negv);
             const float2 pp = make_float2(ex2(x.x), ex2(x.y));
             if (i & 1) sb = fadd2(sb, pp);
@@ -1093,23 +1120,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[i] = pack_bf16x2(pp.x, pp.y);
           }
           l += (sa.x + sb.x) + (sa.y + sb.y);
-          tmem_st16(tS + (c0 >> 1), pk);
-          if (c0 & 32) {   // a half is written: the MMA warp starts on the first meanwhile
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(c0 < 64 ? BAR_PH(t) : BAR_PR(t));
-            // row tile 1 starts a wide segment when tile 0 is here in its first step, so that one tile's products run under
-            // the other's softmax; started together they stay together (5000 cycles a step instead of XX)
-            if (c0 < 64 && first && sg.wide && t == 0 && lane == 0) mbar_arrive(BAR_ST);
-          }
+          tmem_st32(tS + h * 64, pk);
+          tmem_wait_st();
+          if (!(ok = product_done())) break;
+          tc_fence_before();
+          mbar_arrive(BAR_PR(t, h));
+          due = true;
         }
       }
       if (!ok) break;
       // ---- the partial: O / l and m scale + ln l, in fp32
-      ok = wait_all(BAR_OD(t), held & 1u, status, abort_flag);
-      tc_fence_after();
-      if (!ok) break;
-      ++held;
+      if (!(ok = product_done())) break;
       if (warp_live) {
         const size_t slot = static_cast<size_t>(sg.slot);
         const float inv = (l > 0.f) ? 1.f / l : 0.f;
