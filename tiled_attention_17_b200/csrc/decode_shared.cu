@@ -67,16 +67,27 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, unsigned
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Eight 32-bit columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+// Eight, or four, 32-bit columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr)
                : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
                : "memory");
 }
 // Largest of a value over the warp (one instruction on sm_100a).
@@ -266,9 +277,9 @@ struct AttendLayout {
   static constexpr int kSeg = kV + kVStages * kTileBytes;
   static constexpr int kRed = kSeg + kSegments * static_cast<int>(sizeof(Segment));   // [row tile][2][4 warps][8] floats
   static constexpr int kBar = kRed + 2 * 2 * 4 * 8 * 4;
-  // k_full, k_empty, v_full, v_empty; per row tile: s_full[2], p_ready[2], o_free, o_done, exchange, own s_full[2], q_full[]; segment full, empty;
+  // k_full, k_empty, v_full, v_empty; per row tile: s_full[2], p_ready[2], o_free, o_done[2], exchange, own s_full[2], q_full[]; segment full, empty;
   // mma_done, windows read
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 18 + 2 * kQLoads + 2 * kSegments + 2;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 20 + 2 * kQLoads + 2 * kSegments + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag, status word; line's cost, CTA's share
   // slack to align the base to 1024 B; with d = 64 the own-keys product reads 64 rows it does not need, 1 KB on
   static constexpr int kAlloc = kMisc + 32 + 1024 + (D == 64 ? 1024 : 0);
@@ -278,7 +289,8 @@ struct AttendLayout {
   static constexpr uint32_t kTmS0 = 0, kTmS1 = 128, kTmO0 = 256, kTmO1 = 256 + D;
 };
 
-template <int D>
+// kG: query rows own keys are worked on with, Hq / Hkv rounded up to 4 or 8.
+template <int D, int kG>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
   constexpr uint32_t KS = L::kKStages, VS = L::kVStages;
-  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (18 + 2 * kQLoads);
+  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (20 + 2 * kQLoads);
   auto BAR_KF = [&](uint32_t s) { return bar0 + 8u * s; };
   auto BAR_KE = [&](uint32_t s) { return bar0 + 8u * (KS + s); };
   auto BAR_VF = [&](uint32_t s) { return bar0 + 8u * (2 * KS + s); };
@@ -297,10 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto BAR_SF = [&](int t, int h) { return bar_t + 8u * (2 * t + h); };
   auto BAR_PR = [&](int t, int h) { return bar_t + 8u * (4 + 2 * t + h); };
   auto BAR_OF = [&](int t) { return bar_t + 8u * (8 + t); };
-  auto BAR_OD = [&](int t) { return bar_t + 8u * (10 + t); };
-  auto BAR_X = [&](int t) { return bar_t + 8u * (12 + t); };
-  auto BAR_SO = [&](int t, uint32_t k) { return bar_t + 8u * (14 + 2 * t + (k & 1u)); };
-  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (18 + t * kQLoads + load % kQLoads); };
+  auto BAR_OD = [&](int t, uint32_t h) { return bar_t + 8u * (10 + 2 * t + (h & 1u)); };
+  auto BAR_X = [&](int t) { return bar_t + 8u * (14 + t); };
+  auto BAR_SO = [&](int t, uint32_t k) { return bar_t + 8u * (16 + 2 * t + (k & 1u)); };
+  auto BAR_QF = [&](int t, uint32_t load) { return bar_t + 8u * (20 + t * kQLoads + load % kQLoads); };
   auto BAR_GF = [&](uint32_t e) { return bar_s + 8u * e; };
   auto BAR_GE = [&](uint32_t e) { return bar_s + 8u * (kSegments + e); };
   const uint32_t BAR_FIN = bar_s + 8u * 2 * kSegments, BAR_GO = BAR_FIN + 8u;
@@ -335,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(BAR_PR(t, h), 128);
       }
       mbar_init(BAR_OF(t), 128);
-      mbar_init(BAR_OD(t), 1);
+      mbar_init(BAR_OD(t, 0), 1);
+      mbar_init(BAR_OD(t, 1), 1);
       mbar_init(BAR_X(t), 4);   // one lane of each softmax warp
       mbar_init(BAR_SO(t, 0), 1);
       mbar_init(BAR_SO(t, 1), 1);
@@ -680,8 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // page-major V: 16-key step kk starts at byte 2048 (kk + (kk & vmask))
       const int vmask = ~(max(ps / 16, 1) - 1);
       bool ok = true;
-      // steps and segments of this row tile, and products with V taken: S/P, Q/O and o_done barrier phases
-      uint32_t steps_t = 0, used = 0, products = 0;
+      uint32_t steps_t = 0, used = 0;   // steps and segments of this row tile: S/P/o_done and Q/O barrier phases
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
         if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, status, abort_flag))) break;
@@ -748,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mma_ss(tO, a0 + static_cast<uint64_t>(off >> 4), b0 + (kk >> 2) * (kOwnCols * 128 >> 4) + (kk & 3) * 2,
                          idesc_o, (!pfirst || kk > 0) ? 1u : 0u);
                 }
-                mma_commit(BAR_OD(t));
+                mma_commit(BAR_OD(t, k - 1));
                 mma_commit(BAR_VE(vs));
                 mbar_arrive(BAR_VE(vs));
               }
@@ -826,10 +838,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mma_ts(tO, tS + h * 64 + c * 8, b0 + static_cast<uint64_t>(off >> 4), idesc_pv,
                          (j > first || kk > 0) ? 1u : 0u);
                 }
-                mma_commit(BAR_OD(t));
+                mma_commit(BAR_OD(t, h));
               }
               __syncwarp();
-              if (!(ok = wait_all(BAR_OD(t), products++ & 1u, status, abort_flag))) break;
+              if (!(ok = wait_all(BAR_OD(t, h), steps_t & 1u, status, abort_flag))) break;
             }
             // the next step's scores: of this half if K is there, else both later
             const uint32_t kf = BAR_KF(gs % KS), kph = (gs / KS) & 1u;
@@ -870,15 +882,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + (t == 0 ? L::kTmO0 : L::kTmO1) + lane_off;
     const float c2 = a.scale_log2;
     bool ok = true;
-    uint32_t steps_t = 0, held = 0, exchanges = 0, own_k = 0;   // S/P and o_done phases of this row tile; own-keys steps
-    // Waits for the last product with V this row tile's weights went into.  Every
-    // one is waited for, and before the weights of the next are handed over: a
-    // barrier tells only the parity of its phase, so none may be skipped.
-    bool due = false;
-    auto product_done = [&]() {
-      if (!due) return true;
-      due = false;
-      const bool done = wait_all(BAR_OD(t), held++ & 1u, status, abort_flag);
+    uint32_t steps_t = 0, held0 = 0, held1 = 0, exchanges = 0, own_k = 0;   // S/P and o_done phases; own-keys steps
+    // Products with V complete in turn on two barriers (halves of a step; own keys:
+    // every other step).  The scores of a half are formed when the product before on
+    // the same barrier is complete, so at most one phase of each is open and its
+    // parity says which.
+    auto product_done = [&](uint32_t h) {   // the last product on barrier h, and all before it
+      const bool done = wait_all(BAR_OD(t, h), ((h & 1u ? held1 : held0) - 1) & 1u, status, abort_flag);
       tc_fence_after();
       return done;
     };
@@ -916,7 +926,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (own) {
         // ---- own keys: this thread has key `lane_row` of the tile and one score per query row
-        constexpr int kG = 8;
         const int G = a.G;
         float m[kG], l[kG];
 #pragma unroll
@@ -925,12 +934,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           l[i] = 0.f;
         }
         // eight values of each of the row tile's four warps, joined through shared memory
-        float* red = reinterpret_cast<float*>(smem + L::kRed) + t * 2 * 4 * kG;
+        float* red = reinterpret_cast<float*>(smem + L::kRed) + t * 2 * 4 * 8;
         auto exchange = [&](float (&v)[kG], auto join) {
           float* buf = red + (exchanges & 1u) * 4 * kG;   // two in turn: one barrier an exchange
           if (lane == 0) {
-            reinterpret_cast<float4*>(buf + quarter * kG)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(buf + quarter * kG)[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+            for (int i = 0; i < kG; i += 4)
+              *reinterpret_cast<float4*>(buf + quarter * kG + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             mbar_arrive(BAR_X(t));
           }
           if (!wait_all(BAR_X(t), exchanges++ & 1u, status, abort_flag)) return false;
@@ -956,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           uint32_t sr[kG];
-          tmem_ld8(tS + (own_k & 1u) * kOwnCols, sr);
+          tmem_ld(tS + (own_k & 1u) * kOwnCols, sr);
           const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
           const bool is_key = lane_row >= lo && lane_row < lim;
           if ((lim < kTile || lo > 0) && !(ok = zero_values(j, lo, lim))) break;
@@ -981,13 +991,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               l[i] *= alpha[i];
             }
             if (!first) {   // O holds the products of the steps before, once the last of them is done
-              if (!(ok = product_done())) break;
+              if (!(ok = product_done(own_k + 1))) break;   // the step before
               uint32_t orr[kG];
-              tmem_ld8(tO, orr);
+              tmem_ld(tO, orr);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < kG; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha[i]);
-              tmem_st8(tO, orr);
+              tmem_st(tO, orr);
               tmem_wait_st();
             }
           }
@@ -1002,18 +1012,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           weigh(0);
           if (G > 1) weigh(1);
           if (G > 2) {
-            weigh(2);
-            weigh(3);
-          }
-          if (G > 4) {
 #pragma unroll
-            for (int i = 4; i < kG; ++i) weigh(i);
+            for (int i = 2; i < kG; ++i) weigh(i);
           }
           fence_proxy_async_smem();   // P (and zeroed V) before the products read them
-          if (!(ok = product_done())) break;
+          ++(own_k & 1u ? held1 : held0);
           tc_fence_before();
           mbar_arrive(BAR_PR(t, 0));
-          due = true;
         }
         if (!ok) break;
         // ---- the partial: this thread has column `lane_row` of d
@@ -1023,9 +1028,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 16; x >= 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
           }
-        if (!(ok = exchange(l, [](float x, float y) { return x + y; }) && product_done())) break;
+        if (!(ok = exchange(l, [](float x, float y) { return x + y; }) && product_done(own_k + 1))) break;
         uint32_t orr[kG];
-        tmem_ld8(tO, orr);
+        tmem_ld(tO, orr);
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(BAR_OF(t));
@@ -1051,14 +1056,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_all(BAR_SF(t, h), steps_t & 1u, status, abort_flag);
           if (!ok) break;
           tc_fence_after();
+          ++(h ? held1 : held0);   // this half's product is a phase of its barrier
           if (need_mask && h == 0) {
             if (!(ok = zero_values(j, lo, lim))) break;
             fence_proxy_async_smem();
           }
           if (!warp_live) {   // no row of this warp counts: its P may hold anything
-            if (!(ok = product_done())) break;
             mbar_arrive(BAR_PR(t, h));
-            due = true;
             continue;
           }
           uint32_t sr[2][32];
@@ -1091,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
             l *= alpha;
             if (!first) {   // O holds the products of the halves before, once the last of them is done
-              if (!(ok = product_done())) break;
+              if (!(ok = product_done(h ^ 1))) break;
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t orr[32];
@@ -1122,15 +1126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += (sa.x + sb.x) + (sa.y + sb.y);
           tmem_st32(tS + h * 64, pk);
           tmem_wait_st();
-          if (!(ok = product_done())) break;
           tc_fence_before();
           mbar_arrive(BAR_PR(t, h));
-          due = true;
         }
       }
       if (!ok) break;
       // ---- the partial: O / l and m scale + ln l, in fp32
-      if (!(ok = product_done())) break;
+      if (!(ok = product_done(1))) break;
       if (warp_live) {
         const size_t slot = static_cast<size_t>(sg.slot);
         const float inv = (l > 0.f) ? 1.f / l : 0.f;
@@ -1299,7 +1301,7 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, bool 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D>
+template <int D, int kG>
 ta_status launch_attend(const void* q, const void* k_cache, const void* v_cache, const SharedArgs& a,
                         cudaStream_t stream) {
   using L = AttendLayout<D>;
@@ -1328,9 +1330,9 @@ ta_status launch_attend(const void* q, const void* k_cache, const void* v_cache,
     if ((st = encode_bf16_tiled(&tv, v_cache, 5, dv, sv, bv)) != TA_OK) return st;
   }
   static int attr_done[64] = {0};
-  cudaError_t e = ensure_smem_limit(shared_attend_kernel<D>, L::kAlloc, attr_done);
+  cudaError_t e = ensure_smem_limit(shared_attend_kernel<D, kG>, L::kAlloc, attr_done);
   if (e != cudaSuccess) return fail(TA_ERR_CUDA, "shared decode: shared-memory limit", e);
-  e = launch(shared_attend_kernel<D>, dim3(static_cast<unsigned>(a.n_ctas)), kThreads, L::kAlloc, false, stream, tq, tq1,
+  e = launch(shared_attend_kernel<D, kG>, dim3(static_cast<unsigned>(a.n_ctas)), kThreads, L::kAlloc, false, stream, tq, tq1,
              tk, tv, a);
   return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: attend kernel launch", e);
 }
@@ -1412,8 +1414,9 @@ ta_status launch_decode_shared(const void* q, const void* k_cache, const void* v
   a.own_o = reinterpret_cast<float*>(ws + plan.own_o);
   a.own_lse = reinterpret_cast<float*>(ws + plan.own_lse);
 
-  const ta_status st = d == 128 ? launch_attend<128>(q, k_cache, v_cache, a, stream)
-                                : launch_attend<64>(q, k_cache, v_cache, a, stream);
+  const bool four = a.G <= 4;
+  const ta_status st = d == 128 ? (four ? launch_attend<128, 4> : launch_attend<128, 8>)(q, k_cache, v_cache, a, stream)
+                                : (four ? launch_attend<64, 4> : launch_attend<64, 8>)(q, k_cache, v_cache, a, stream);
   if (st != TA_OK) return st;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(o);
   const cudaError_t e = d == 128 ? launch_combine<128>(a, out, lse, stream) : launch_combine<64>(a, out, lse, stream);
