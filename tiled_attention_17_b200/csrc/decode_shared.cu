@@ -23,8 +23,8 @@
 //
 // Work.  An item is a group's prefix or a sequence's own keys; a unit is (item,
 // KV head, block of 256 query rows); its steps are 128-key tiles.  All units'
-// steps are laid end to end, a step that serves more than 128 rows counting
-// kWideCost, others 1, and CTA c of n takes the steps that start in
+// steps are laid end to end, each as long as its cost (more with more than 128
+// rows), and CTA c of n takes the steps that start in
 // [c L, (c + 1) L), L = ceil(total / n): equal shares whatever the groups' sizes
 // and lengths, at the price of partial results per CTA and unit it touches.
 // The (c, unit) pairs met along the line are monotone in both, so slot
@@ -49,8 +49,11 @@ constexpr int kUnitRows = 2 * kTile;
 constexpr int kThreads = 416;
 constexpr int kSoftmaxWarp0 = 4, kMmaWarp1 = 12;
 constexpr float kRescaleLog2 = 8.0f;   // the stale-max margin of the prefill kernel
-constexpr int kWideShift = 1;          // a step with two row tiles costs 2^kWideShift, one with a single tile 1
-constexpr int kWideCost = 1 << kWideShift;
+// Cost of a step with two row tiles, and with one.  Measured 2.33 us (256 samples
+// behind 30000 shared tokens: both tiles' softmax) and 1.36 us (their own tokens,
+// segments of one or two steps: latency); at 2 : 1 the last CTA ended 17% after
+// the median.
+constexpr int kWideCost = 5, kNarrowCost = 3;
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -119,7 +122,7 @@ struct __align__(16) SeqPlan {
 
 __host__ __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __host__ __device__ __forceinline__ int blocks_of(int n, int G) { return (n * G + kUnitRows - 1) / kUnitRows; }   // of rows
-__host__ __device__ __forceinline__ int shift_of(int n, int G) { return n * G > kTile ? kWideShift : 0; }   // log2 cost of a step
+__host__ __device__ __forceinline__ int cost_of(int n, int G) { return n * G > kTile ? kWideCost : kNarrowCost; }   // of a step
 
 struct SharedArgs {
   const int32_t* block_table;
@@ -198,7 +201,7 @@ __device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int 
     prefetch_l2(a.block_table + static_cast<size_t>(r.it.first) * a.max_pages + r.it.base / a.page_size);
   const int tiles = tiles_of(r.it.end - r.it.base);
   const int units = tiles > 0 ? blocks_of(r.it.n, a.G) * a.Hkv : 0, own_units = i < groups ? units : 0;
-  r.cost = (static_cast<long long>(units) * tiles) << shift_of(r.it.n, a.G);
+  r.cost = static_cast<long long>(units) * tiles * cost_of(r.it.n, a.G);
   long long sum = r.cost;
   int sum_u = own_units;
 #pragma unroll
@@ -217,12 +220,17 @@ __device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int 
   return r;
 }
 
-// Steps of a unit that start in CTA c's share: [j0, j1) of `tiles`, x0 the
-// unit's place on the line, 2^shift the cost of a step.
-__device__ __forceinline__ void unit_share(long long x0, int tiles, int shift, long long per, int c, int& j0, int& j1) {
-  const long long a = per * c - x0, b = a + per, up = (1 << shift) - 1;
-  j0 = a <= 0 ? 0 : static_cast<int>((a + up) >> shift);
-  const long long e = (b + up) >> shift;
+// x / cost rounded up, x >= 0 (divisions by constants).
+__device__ __forceinline__ long long steps_in(long long x, int cost) {
+  const unsigned long long u = static_cast<unsigned long long>(x);
+  return static_cast<long long>(cost == kWideCost ? (u + (kWideCost - 1)) / kWideCost : (u + (kNarrowCost - 1)) / kNarrowCost);
+}
+// Steps of a unit that start in CTA c's share (which reaches into the unit):
+// [j0, j1) of `tiles`, x0 the unit's place on the line, `cost` a step's.
+__device__ __forceinline__ void unit_share(long long x0, int tiles, int cost, long long per, int c, int& j0, int& j1) {
+  const long long a = per * c - x0;
+  j0 = a <= 0 ? 0 : static_cast<int>(steps_in(a, cost));
+  const long long e = steps_in(a + per, cost);
   j1 = e < tiles ? static_cast<int>(e) : tiles;
 }
 
@@ -325,7 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_launch_dependents();   // the combine kernel waits for this grid before it reads anything
   // the plan's inputs on their way into L2 while barriers and tensor memory are set up (32 numbers a line)
+#pragma unroll 1
   for (int i = threadIdx.x * 32; i < a.num_seqs; i += kThreads * 32) prefetch_l2(a.seq_lens + i);
+#pragma unroll 1
   for (int i = threadIdx.x * 32; i < a.num_groups; i += kThreads * 32) {
     prefetch_l2(a.group_offsets + i);
     prefetch_l2(a.prefix_lens + i);
@@ -377,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // numbers a sequence, and a kernel of its own for them cost 8 us.
   // Groups that decrease or leave the batch might overlap: then none is used.
   bool bad = false;
+#pragma unroll 1
   for (int g = threadIdx.x; g < a.num_groups; g += kThreads) {
     const int lo = __ldg(a.group_offsets + g), hi = __ldg(a.group_offsets + g + 1);
     bad = bad || lo < 0 || hi < lo || hi > a.num_seqs;
@@ -386,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int groups = ignore ? 0 : a.num_groups, n_items = groups + a.num_seqs, n_windows = (n_items + 31) / 32;
   long long* wx = reinterpret_cast<long long*>(smem + L::kK);   // cost, then place, of each window of 32 items
   int* wu = reinterpret_cast<int*>(wx + kMaxWindows);
+#pragma unroll 1
   for (int w = warp; w < n_windows; w += kThreads / 32) {
     long long cost = 0;
     int units = 0;
@@ -400,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {   // sums before each window
     long long base = 0;
     int base_u = 0;
+#pragma unroll 1
     for (int w0 = 0; w0 < n_windows; w0 += 32) {
       const int w = w0 + lane;
       const long long c = w < n_windows ? wx[w] : 0;
@@ -447,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(BAR_GO);
     __syncwarp();
+#pragma unroll 1
     for (int k = 0, w = static_cast<int>(blockIdx.x); w < n_windows; ++k, w += a.n_ctas) {
       long long base = __shfl_sync(0xffffffffu, at, k);
       int base_u = __shfl_sync(0xffffffffu, at_u, k);
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Window win = {};
       Item it = {};
       uint32_t work = 0;
-      int unit = 0, tiles = 0, blocks = 1, shift = 0;
+      int unit = 0, tiles = 0, blocks = 1, cost = 1;
       bool own = false;
       long long ux = end;
       auto enter = [&](int lane_of) {   // the item of a lane of the window
@@ -488,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         own = w * 32 + lane_of >= groups;
         tiles = tiles_of(it.end - it.base);
         blocks = blocks_of(it.n, a.G);
-        shift = shift_of(it.n, a.G);
+        cost = cost_of(it.n, a.G);
         unit = 0;
         ux = it.x0;
       };
@@ -498,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (begin < end) {
         int lo = 0, n = n_windows;   // the last window that starts at or before `begin`: a 32-way search
+#pragma unroll 1
         while (n > 1) {
           const int step = (n + 31) / 32, at = lane * step;
           const uint32_t le = __ballot_sync(0xffffffffu, at < n && wx[lo + at] <= begin);
@@ -511,12 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         next_window();
         // and in it the last item with work that does
         enter(31 - __clz(__ballot_sync(0xffffffffu, win.cost > 0 && win.it.x0 <= begin)));
-        const long long unit_cost = static_cast<long long>(tiles) << shift, in = begin - ux;
+        const long long unit_cost = static_cast<long long>(tiles) * cost, in = begin - ux;
         unit = static_cast<int>(in <= UINT32_MAX ? static_cast<unsigned>(in) / static_cast<unsigned>(unit_cost) : in / unit_cost);
         ux += unit * unit_cost;
       }
       auto advance = [&]() {   // to the next unit, if the share reaches it
-        ux += static_cast<long long>(tiles) << shift;
+        ux += static_cast<long long>(tiles) * cost;
         if (ux < end && ++unit == blocks * a.Hkv) {
           while (work == 0) {
             ++w;
@@ -527,10 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t g0 = 0;
       int turn = 0;   // row tile that takes the next narrow step
+#pragma unroll 1
       for (uint32_t n = 0;; ++n) {
         int j0 = 0, j1 = 0;
+#pragma unroll 1
         while (ux < end) {
-          unit_share(ux, tiles, shift, per, static_cast<int>(blockIdx.x), j0, j1);
+          unit_share(ux, tiles, cost, per, static_cast<int>(blockIdx.x), j0, j1);
           if (j0 < j1) break;   // else the share begins inside the unit's last step
           advance();
         }
@@ -596,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t qlast[2] = {0, 0};   // ring position of the last step that reads each
       bool qown[2] = {false, false};
       bool ok = true;
+#pragma unroll 1
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
         if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, status, abort_flag))) break;
@@ -610,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(BAR_GE(e));
         if (tiles == 0) break;
         // queries: narrow segments of several steps keep the same rows in both buffers
+#pragma unroll 1
         for (int t = 0; t < 2 && !is_v; ++t) {
           if (!wide && tiles == 1 && t != tile_first) continue;
           // A whole tile, or rows after one, wait until the scores of the last step that reads the buffer are formed:
@@ -638,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         // key tiles.  A page arrives in one copy in the 128-byte swizzle: K as [8-row
         // group][64-column chunk][8 rows][128 B], V as [chunk][page rows][128 B].
+#pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
           int pg_next = -1;   // under way before the wait
           const int p = (j + 1) * per_tile + lane;
@@ -665,9 +685,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // drain: no copy into this CTA's shared memory may still be in flight at exit
       if (lane == 0) {
+#pragma unroll 1
         for (int t = 0; t < 2; ++t)
+#pragma unroll 1
           for (uint32_t u = qn[t] > kQLoads ? qn[t] - kQLoads : 0u; u < qn[t]; ++u)
             mbar_wait(BAR_QF(t, u), (u / kQLoads) & 1u, nullptr, nullptr, kWaitLimitNs);
+#pragma unroll 1
         for (uint32_t k = 0; k < stages; ++k)   // the last fill of each slot
           if (use > 0 || k < slot)
             mbar_wait(full0 + 8u * k, (k < slot ? use : use - 1) & 1u, nullptr, nullptr, kWaitLimitNs);
@@ -694,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vmask = ~(max(ps / 16, 1) - 1);
       bool ok = true;
       uint32_t steps_t = 0, used = 0;   // steps and segments of this row tile: S/P/o_done and Q/O barrier phases
+#pragma unroll 1
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t e = n % kSegments;
         if (!(ok = wait_all(BAR_GF(e), (n / kSegments) & 1u, status, abort_flag))) break;
@@ -892,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return done;
     };
+#pragma unroll 1
     for (uint32_t seg = 0; ok; ++seg) {
       const uint32_t e = seg % kSegments;
       ok = wait_all(BAR_GF(e), (seg / kSegments) & 1u, status, abort_flag);
@@ -914,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t gj = sg.g0 + static_cast<uint32_t>(j), sv = gj % VS;
         if (!wait_all(BAR_VF(sv), (gj / VS) & 1u, status, abort_flag)) return false;
         if (lane_row >= lim || lane_row < lo) {
-          const int pr = lane_row % a.page_size;
+          const int pr = lane_row & (a.page_size - 1);
           uint8_t* base = smem + L::kV + sv * L::kTileBytes + (lane_row - pr) * D * 2 + pr * 128;
 #pragma unroll 1
           for (int c = 0; c < L::kChunks; ++c)
@@ -961,6 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint8_t* const prow = smem + L::kQ + t * L::kTileBytes + kOwnP + (lane_row >> 6) * (kOwnCols * 128);
         const uint32_t pcol = static_cast<uint32_t>(((lane_row & 63) >> 3) * 16), pbyte = static_cast<uint32_t>((lane_row & 7) * 2);
+#pragma unroll 1
         for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t, ++own_k) {
           ok = wait_all(BAR_SO(t, own_k), (own_k >> 1) & 1u, status, abort_flag);
           if (!ok) break;
@@ -1047,6 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (bool first = true; j < sg.tiles && ok; j += stride, ++steps_t) {
         // keys of this tile: columns [lo, lim); the rest of its shared memory holds none that count
         const int lo = j == 0 ? sg.lo : 0, lim = min(kTile, sg.hi - j * kTile);
@@ -1184,9 +1211,9 @@ __device__ __forceinline__ long long divide(long long x, long long y) {   // bot
   return ((x | y) >> 32) == 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(y) : x / y;
 }
 // The CTAs [c0, c0 + n) that hold partials of a unit at place x0 on the line.
-__device__ __forceinline__ void unit_ctas(long long x0, int tiles, int shift, long long per, int& c0, int& n) {
+__device__ __forceinline__ void unit_ctas(long long x0, int tiles, int cost, long long per, int& c0, int& n) {
   c0 = static_cast<int>(divide(x0, per));
-  n = static_cast<int>(divide(x0 + (static_cast<long long>(tiles - 1) << shift), per)) - c0 + 1;
+  n = static_cast<int>(divide(x0 + static_cast<long long>(tiles - 1) * cost, per)) - c0 + 1;
 }
 
 template <int D, int G>
@@ -1201,17 +1228,17 @@ __global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedA
   bool wide = true;
   if (sp.group >= 0) {
     const GroupPlan g = a.groups[sp.group];
-    const int blocks = blocks_of(g.n, G), shift = shift_of(g.n, G);
+    const int blocks = blocks_of(g.n, G), cost = cost_of(g.n, G);
     const int r = (seq - g.first) * G, block = r / kUnitRows, unit = hkv * blocks + block;
     wide = min(kUnitRows, g.n * G - block * kUnitRows) > kTile;
     int c0;
-    unit_ctas(g.x0 + ((static_cast<long long>(unit) * g.tiles) << shift), g.tiles, shift, per, c0, n_pre);
+    unit_ctas(g.x0 + static_cast<long long>(unit) * g.tiles * cost, g.tiles, cost, per, c0, n_pre);
     pre0 = static_cast<size_t>(c0 + g.unit0 + unit) * kUnitRows + r % kUnitRows + gq;
     if (!wide) n_pre *= 2;
   }
   if (sp.tiles > 0) {
     int c0;
-    unit_ctas(sp.x0 + static_cast<long long>(hkv) * sp.tiles, sp.tiles, 0, per, c0, n_own);
+    unit_ctas(sp.x0 + static_cast<long long>(hkv) * sp.tiles * kNarrowCost, sp.tiles, kNarrowCost, per, c0, n_own);
     own0 = static_cast<size_t>(c0 + seq * a.Hkv + hkv) * 2 * G + gq;
     n_own *= 2;
   }
