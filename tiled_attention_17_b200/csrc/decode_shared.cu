@@ -53,7 +53,10 @@ constexpr float kRescaleLog2 = 8.0f;   // the stale-max margin of the prefill ke
 // behind 30000 shared tokens: both tiles' softmax) and 1.36 us (their own tokens,
 // segments of one or two steps: latency); at 2 : 1 the last CTA ended 17% after
 // the median.
-constexpr int kWideCost = 5, kNarrowCost = 3;
+// A further unit with wide steps costs a CTA some 4 us more than the steps (its
+// partial is 128 KB, and the pipeline starts again): without a cost of its own the
+// CTAs with two of them ended 25% after the median of a small batch.
+constexpr int kWideCost = 5, kNarrowCost = 3, kWideStart = 8;
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -123,6 +126,11 @@ struct __align__(16) SeqPlan {
 __host__ __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __host__ __device__ __forceinline__ int blocks_of(int n, int G) { return (n * G + kUnitRows - 1) / kUnitRows; }   // of rows
 __host__ __device__ __forceinline__ int cost_of(int n, int G) { return n * G > kTile ? kWideCost : kNarrowCost; }   // of a step
+// A unit's length on the line: what it costs to start, then its steps.
+__host__ __device__ __forceinline__ int start_of(int cost) { return cost == kWideCost ? kWideStart : 0; }
+__host__ __device__ __forceinline__ long long unit_cost(int tiles, int cost) {
+  return tiles > 0 ? static_cast<long long>(tiles) * cost + start_of(cost) : 0;
+}
 
 struct SharedArgs {
   const int32_t* block_table;
@@ -201,7 +209,7 @@ __device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int 
     prefetch_l2(a.block_table + static_cast<size_t>(r.it.first) * a.max_pages + r.it.base / a.page_size);
   const int tiles = tiles_of(r.it.end - r.it.base);
   const int units = tiles > 0 ? blocks_of(r.it.n, a.G) * a.Hkv : 0, own_units = i < groups ? units : 0;
-  r.cost = static_cast<long long>(units) * tiles * cost_of(r.it.n, a.G);
+  r.cost = units * unit_cost(tiles, cost_of(r.it.n, a.G));
   long long sum = r.cost;
   int sum_u = own_units;
 #pragma unroll
@@ -226,11 +234,12 @@ __device__ __forceinline__ long long steps_in(long long x, int cost) {
   return static_cast<long long>(cost == kWideCost ? (u + (kWideCost - 1)) / kWideCost : (u + (kNarrowCost - 1)) / kNarrowCost);
 }
 // Steps of a unit that start in CTA c's share (which reaches into the unit):
-// [j0, j1) of `tiles`, x0 the unit's place on the line, `cost` a step's.
+// [j0, j1) of `tiles`, x0 the unit's place on the line, `cost` a step's.  None
+// where the share ends before the first, or begins inside the last.
 __device__ __forceinline__ void unit_share(long long x0, int tiles, int cost, long long per, int c, int& j0, int& j1) {
-  const long long a = per * c - x0;
+  const long long a = per * c - x0 - start_of(cost);
   j0 = a <= 0 ? 0 : static_cast<int>(steps_in(a, cost));
-  const long long e = steps_in(a + per, cost);
+  const long long e = a + per <= 0 ? 0 : steps_in(a + per, cost);
   j1 = e < tiles ? static_cast<int>(e) : tiles;
 }
 
@@ -526,12 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         next_window();
         // and in it the last item with work that does
         enter(31 - __clz(__ballot_sync(0xffffffffu, win.cost > 0 && win.it.x0 <= begin)));
-        const long long unit_cost = static_cast<long long>(tiles) * cost, in = begin - ux;
-        unit = static_cast<int>(in <= UINT32_MAX ? static_cast<unsigned>(in) / static_cast<unsigned>(unit_cost) : in / unit_cost);
-        ux += unit * unit_cost;
+        const long long length = unit_cost(tiles, cost), in = begin - ux;
+        unit = static_cast<int>(in <= UINT32_MAX ? static_cast<unsigned>(in) / static_cast<unsigned>(length) : in / length);
+        ux += unit * length;
       }
       auto advance = [&]() {   // to the next unit, if the share reaches it
-        ux += static_cast<long long>(tiles) * cost;
+        ux += unit_cost(tiles, cost);
         if (ux < end && ++unit == blocks * a.Hkv) {
           while (work == 0) {
             ++w;
@@ -548,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (ux < end) {
           unit_share(ux, tiles, cost, per, static_cast<int>(blockIdx.x), j0, j1);
-          if (j0 < j1) break;   // else the share begins inside the unit's last step
+          if (j0 < j1) break;   // else the share only touches the unit
           advance();
         }
         const bool done = j0 >= j1;
@@ -1212,6 +1221,7 @@ __device__ __forceinline__ long long divide(long long x, long long y) {   // bot
 }
 // The CTAs [c0, c0 + n) that hold partials of a unit at place x0 on the line.
 __device__ __forceinline__ void unit_ctas(long long x0, int tiles, int cost, long long per, int& c0, int& n) {
+  x0 += start_of(cost);
   c0 = static_cast<int>(divide(x0, per));
   n = static_cast<int>(divide(x0 + static_cast<long long>(tiles - 1) * cost, per)) - c0 + 1;
 }
@@ -1232,7 +1242,7 @@ __global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedA
     const int r = (seq - g.first) * G, block = r / kUnitRows, unit = hkv * blocks + block;
     wide = min(kUnitRows, g.n * G - block * kUnitRows) > kTile;
     int c0;
-    unit_ctas(g.x0 + static_cast<long long>(unit) * g.tiles * cost, g.tiles, cost, per, c0, n_pre);
+    unit_ctas(g.x0 + unit * unit_cost(g.tiles, cost), g.tiles, cost, per, c0, n_pre);
     pre0 = static_cast<size_t>(c0 + g.unit0 + unit) * kUnitRows + r % kUnitRows + gq;
     if (!wide) n_pre *= 2;
   }
