@@ -2,10 +2,10 @@
 GPU, against the definition in 64 bits.
 
 Error bound of one rotated element.  The fraction of a turn is exact in fp64 up
-to 2^-51 of the angle and is rounded once to fp32 (half-turns of at most 1:
-2^-24 of a half-turn, 2 x 10^-7 radians, under 2^-22); sincospi is within 2
-units of the last place (2^-23 each); the amplitude's product, the two
-products and the sum round in fp32 (2^-24 each).  Together under 2^-20 of
+to 2^-51 of the angle; as an angle of at most pi it is rounded twice to fp32
+(2^-24 each: under 2^-21.4 radians together); the hardware's sine and cosine are
+within 2^-21.1 on that range; the amplitude's product, the two products and the
+sum round in fp32 (2^-24 each).  Together under 2^-19.9, taken as 2^-19.5, of
 amp (|a| + |b|), plus 2^-51 |angle| amp (|a| + |b|).  Then one rounding to
 bf16, at most 2^-8 of the value.  Copied elements are equal bit for bit.
 """
@@ -38,7 +38,7 @@ def turned(torch, x, pos, inv_freq, interleaved, amp, sign=1.0):
     c, s = torch.cos(angle), sign * torch.sin(angle)
     y, tol = x.clone(), torch.zeros_like(x)
     y[..., ia], y[..., ib] = amp * (a * c - b * s), amp * (a * s + b * c)
-    t = abs(amp) * (a.abs() + b.abs()) * (2.0 ** -20 + 2.0 ** -51 * angle.abs())
+    t = abs(amp) * (a.abs() + b.abs()) * (2.0 ** -19.5 + 2.0 ** -51 * angle.abs())
     tol[..., ia] = t + y[..., ia].abs() * 2.0 ** -8
     tol[..., ib] = t + y[..., ib].abs() * 2.0 ** -8
     return y, tol

@@ -11,7 +11,8 @@
 // The angle of a far position needs more than 32 bits (p = 10^6 at one radian
 // a token leaves 0.06 rad of error in fp32): p * inv_freq / (2 pi) is formed in
 // fp64, whole turns are dropped there, and only the fraction of a turn goes to
-// fp32 (2^-24 of a turn), where sincospi takes it.
+// fp32.  Sine and cosine of at most half a turn then come from the hardware's
+// approximation: within 2^-21 of 1, next to the 2^-9 a bf16 result is rounded by.
 //
 // Bound: HBM bytes, each element read once and written once.  One thread owns
 // 16 elements (8 pairs) of a row and walks over heads of its token with the
@@ -30,7 +31,7 @@
 namespace ta {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kInFlight = 4;      // heads loaded before the first is used
 
 // Eight cosines and sines of pairs [8 u, 8 u + 8) at one position.
@@ -41,13 +42,15 @@ struct Turn {
 __device__ __forceinline__ void make_turn(Turn& t, int position, const double* __restrict__ inv_freq, int u,
                                           float amp, float sign) {
   constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
-  const double p = static_cast<double>(position) * kPerTurn;
+  constexpr double kRound = 6755399441055744.0;         // 1.5 * 2^52: adding and taking it off rounds to an integer
+  constexpr float kTwoPi = 6.28318530717958647693f;
+  const double p = static_cast<double>(position) * kPerTurn;   // |p f| < 2^51 for every int32 position and f < 2^20
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    double turns = p * __ldg(inv_freq + 8 * u + e);
-    turns -= rint(turns);
+    const double turns = p * __ldg(inv_freq + 8 * u + e);
+    const float angle = static_cast<float>(turns - ((turns + kRound) - kRound)) * kTwoPi;
     float s, c;
-    sincospif(static_cast<float>(2.0 * turns), &s, &c);
+    __sincosf(angle, &s, &c);
     t.c[e] = c * amp;
     t.s[e] = s * (amp * sign);
   }
@@ -301,16 +304,17 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
   }
 }
 
-// Heads one thread walks over: as many as leave two full sets of resident
-// threads on every SM (148 SMs x 2048), so that a token's angles are formed as
-// few times as the machine stays filled, and at least one load group.
+// Heads one thread walks over.  More heads share one token's angles (about as much
+// work as three heads), fewer give more threads.  Measured on a B200 (us, 1 / 2 /
+// 4 / 8 heads): forward of 4 x 4096 tokens, 16 + 16 heads of 128: 97 / 61 / 48 / 49;
+// ragged append of 16686 tokens, 48 rows: 167 / 98 / 72 / 76; 3 x 1021 tokens, 6 + 2
+// heads: 10.1 / 8.6 / 8.5 / 9.8; 64 tokens, 48 rows: 4.4 / 4.3 / 4.6 / 7.9.  So one
+// where threads are few enough to run at once with a block a scheduler, two up
+// to a full machine, else four.
 int heads_per_thread(int64_t threads_per_head, int heads) {
-  const int64_t want = 2ll * 148 * 2048;
-  int64_t per = threads_per_head * heads / want;
-  if (per >= heads) per = heads;
-  if (threads_per_head * heads <= want / 4) per = 1;
-  else if (per < kInFlight) per = kInFlight;
-  return static_cast<int>(per < 1 ? 1 : (per > heads ? heads : per));
+  const int64_t threads = threads_per_head * heads;
+  const int per = threads <= 148 * 4 * 64 ? 1 : threads <= 148 * 1024 / 2 ? 2 : 4;
+  return per < heads ? per : heads;
 }
 
 }  // namespace
