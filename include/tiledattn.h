@@ -203,9 +203,9 @@ ta_status attn_lse_merge_finish(const float *acc_o, void *out, int64_t rows, int
  *   positions    int32, element b * pos_stride_b + n for token n of batch b
  *                (pos_stride_b = 0: one row for all batches); may be
  *                negative.  NULL: position n.
- *   inv_freq     [rotary_dim / 2] fp64, radians per position (any scaling for
- *                long contexts is in these and the amplitude).  May be NULL if
- *                rotary_dim is 0 (then the call only copies).
+ *   inv_freq     [rotary_dim / 2] fp64, radians per position, below 2^20 (any
+ *                scaling for long contexts is in these and the amplitude).  May
+ *                be NULL if rotary_dim is 0 (then the call only copies).
  *
  * Supported: d in {64, 128}, rotary_dim a multiple of 16 in [0, d], B * N <
  * 2^31, H <= 65535, amplitude finite.  B * H * N == 0 does nothing.
@@ -251,7 +251,8 @@ ta_status attn_rope(const void *x, void *y, const int32_t *positions, const doub
  * offset writes nothing, one with a bad page writes its q_out row only.  Two
  * tokens whose table entries name the same slot race.  Supported: d in {64,
  * 128}, page_size in {8, 16, 32, 64}, rotary_dim a multiple of 16 in [0, d],
- * Hq + 2 Hkv <= 65535, max_pages * page_size <= 2^30.  Allocates nothing.
+ * Hq + 2 Hkv <= 65535, max_pages * page_size <= 2^30, total <= 2^30.
+ * Allocates nothing.
  */
 ta_status attn_paged_append(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
                             const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *seq_lens,
@@ -399,10 +400,11 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
  *                after the prefix; all of them where there is none), at most
  *                max_pages * page_size.  A sequence with more is cut there and
  *                flagged: a wrong length or prefix costs no more than that
- *   workspace    >= attn_paged_decode_shared_workspace_size(...) bytes,
- *                256-byte aligned, as in attn_paged_decode; the status word is
- *                read by attn_paged_decode_check.  Must not be shared by calls
- *                that may run concurrently
+ *   workspace    >= attn_paged_decode_shared_workspace_size(...) bytes (asked
+ *                with the device current that the call will run on: partials
+ *                are kept for each of its SMs), 256-byte aligned; the status
+ *                word is read by attn_paged_decode_check.  Must not be shared
+ *                by calls that may run concurrently
  *
  * Supported: the shapes of attn_paged_decode, max_pages * page_size <= 2^30,
  * num_groups <= 65535, num_pages_total * Hkv < 2^31.  Pool rows behind a

@@ -235,6 +235,49 @@ def test_shared_repeats_bit_for_bit(cuda):
         assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("G,d", [(4, 128), (8, 64), (1, 128), (2, 64)])
+def test_shared_many_short_segments(cuda, G, d):
+    # hundreds of sequences with one or two tiles of their own behind a prefix cut over every SM: row tiles that run
+    # far apart, partials of one and of two steps, the same bits every time
+    torch, binding = cuda
+    own = [(37 * i) % 260 for i in range(200)]
+    b = Batch(torch, [(1500, own[:150]), (90, own[150:])], 4 * G, 4, d, 16, seed=G + d)
+    first = b.run(torch, binding)
+    check(torch, first, b.expect(torch), f"G{G} d{d}")
+    for _ in range(20):
+        o, lse, flags = b.run(torch, binding)
+        assert flags == 0 and torch.equal(o.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
+
+
+def test_shared_large_batches(cuda):
+    # thousands of sequences in more than a thousand groups (the plan's windows and searches), whose tables hold
+    # whole prefixes: the ordinary decode gives the same result on the same pages
+    torch, binding = cuda
+    S, ps, Hq, Hkv, d = 6000, 16, 2, 1, 64
+    sizes = [(i * 7) % 11 for i in range(1200)]           # some empty
+    g = torch.Generator().manual_seed(3)
+    pages = torch.randint(0, 5000, (S, 12), generator=g, dtype=torch.int32)
+    lens = torch.randint(1, 12 * ps + 1, (S,), generator=g, dtype=torch.int32)
+    lens[::97] = 0
+    offsets, prefix = [5], []
+    for i, n in enumerate(sizes):
+        offsets.append(min(offsets[-1] + n, S))
+        prefix.append(ps * (i % 9))
+        pages[offsets[-2]:offsets[-1], :i % 9] = pages[offsets[-2]:offsets[-2] + 1, :i % 9].clone()
+    q = torch.randn(S, Hq, d, generator=g).to(torch.bfloat16).cuda()
+    kc, vc = (torch.randn(5000, Hkv, ps, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()   # noqa: E731
+    o, lse, ws = binding.paged_decode_shared(q, kc, vc, i32(pages), i32(lens), i32(offsets), i32(prefix))
+    ref, ref_lse, _ = binding.paged_decode(q, kc, vc, i32(pages), i32(lens))
+    assert binding.attn_paged_decode_check(ws) == (0, 0)
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(ref_lse))
+    seen = ~torch.isneginf(ref_lse)
+    assert (lse - ref_lse)[seen].abs().max().item() <= 1e-3
+    # both are within the parity bar of the definition
+    assert (o - ref).float().norm().item() <= 1e-2 * ref.float().norm().item()
+    assert (o - ref).float().abs().max().item() <= 4e-2
+
+
 def test_shared_flags_bad_inputs(cuda):
     torch, binding = cuda
     b = Batch(torch, [(100, [20, 30]), (64, [5])], 4, 1, 64, 16, seed=11, poison=False)

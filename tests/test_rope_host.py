@@ -78,6 +78,7 @@ def test_append_validation(lib):
     assert call(qs=(1024, 128)) == "TA_ERR_INVALID_ARG"    # in place, but q's rows are not q_out's
     assert call(f=None) == "TA_ERR_INVALID_ARG"
     assert call(amp=float("inf")) == "TA_ERR_INVALID_ARG"
+    assert call(T=(1 << 30) + 1) == "TA_ERR_UNSUPPORTED"
     assert call(T=0) == "TA_OK"
     assert call(S=0) == "TA_OK"
 

@@ -330,7 +330,8 @@ ta_status attn_paged_append(const void* q, const void* k, const void* v, void* q
   const ta_status st = validate_rotation(inv_freq, d, rotary_dim, interleaved, amplitude);
   if (st != TA_OK) return st;
   if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64) return TA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_pages) * page_size > (1 << 30) || static_cast<long long>(Hq) + 2ll * Hkv > 65535)
+  if (static_cast<long long>(max_pages) * page_size > (1 << 30) || static_cast<long long>(Hq) + 2ll * Hkv > 65535 ||
+      total > (1 << 30))
     return TA_ERR_UNSUPPORTED;
   if (total == 0 || num_seqs == 0) return TA_OK;
   if (!k || !v || !k_cache || !v_cache || !block_table || !seq_lens || (q && !q_out)) return TA_ERR_INVALID_ARG;
