@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto BAR_VF = [&](uint32_t s) { return bar0 + 8u * (2 * KS + s); };
   auto BAR_VE = [&](uint32_t s) { return bar0 + 8u * (2 * KS + VS + s); };
   auto BAR_SF = [&](int t, int h) { return bar_t + 8u * (2 * t + h); };
-  auto BAR_PR = [&](int t, int h) { return bar_t + 8u * (4 + 2 * t + h); };
+  auto BAR_PR = [&](int t, uint32_t h) { return bar_t + 8u * (4 + 2 * t + h); };
   auto BAR_OF = [&](int t) { return bar_t + 8u * (8 + t); };
   auto BAR_OD = [&](int t, uint32_t h) { return bar_t + 8u * (10 + 2 * t + (h & 1u)); };
   auto BAR_X = [&](int t) { return bar_t + 8u * (14 + t); };
@@ -778,12 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
             }
-            if (k > 0) {   // the product of the step before
+            if (k > 0) {   // the product of the step before, by now the softmax may be a step further: two barriers in turn
               const uint32_t vs = pg % VS;
               if (!(ok = wait_all(BAR_VF(vs), (pg / VS) & 1u, status, abort_flag))) break;
               if (pfirst && pused > 0 && !(ok = wait_all(BAR_OF(t), (pused - 1) & 1u, status, abort_flag))) break;
-              if (!(ok = wait_all(BAR_PR(t, 0), steps_t & 1u, status, abort_flag))) break;
-              ++steps_t;
+              if (!(ok = wait_all(BAR_PR(t, (k - 1) & 1u), (steps_t + ((k - 1) >> 1)) & 1u, status, abort_flag))) break;
               tc_fence_after();
               if (leader) {
                 const uint64_t a0 = dVt + vs * kTileStep, b0 = dP + ((k & 1u) ^ 1u) * (kOwnPBytes >> 4);
@@ -996,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* const prow = smem + L::kQ + t * L::kTileBytes + kOwnP + (lane_row >> 6) * (kOwnCols * 128);
         const uint32_t pcol = static_cast<uint32_t>(((lane_row & 63) >> 3) * 16), pbyte = static_cast<uint32_t>((lane_row & 7) * 2);
 #pragma unroll 1
-        for (bool first = true; j < sg.tiles; j += stride, first = false, ++steps_t, ++own_k) {
+        for (bool first = true; j < sg.tiles; j += stride, first = false, ++own_k) {
           ok = wait_all(BAR_SO(t, own_k), (own_k >> 1) & 1u, status, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -1053,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();   // P (and zeroed V) before the products read them
           ++(own_k & 1u ? held1 : held0);
           tc_fence_before();
-          mbar_arrive(BAR_PR(t, 0));
+          mbar_arrive(BAR_PR(t, own_k & 1u));
         }
         if (!ok) break;
         // ---- the partial: this thread has column `lane_row` of d
