@@ -249,6 +249,34 @@ def test_shared_many_short_segments(cuda, G, d):
         assert flags == 0 and torch.equal(o.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("G,d", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("groups", [[(2000, [1 + (53 * i) % 700 for i in range(64)])],   # narrow prefixes, then own keys
+                                    [(130, [300] * 3), (900, [(91 * i) % 400 for i in range(90)]), (0, [513] * 7)]])
+def test_shared_beside_other_copies(cuda, G, d, groups):
+    # another stream keeps the memory busy, so K and V tiles arrive late and out of step: nothing may depend on it
+    torch, binding = cuda
+    b = Batch(torch, groups, 4 * G, 4, d, 16, seed=G * d)
+    first = b.run(torch, binding)
+    check(torch, first, b.expect(torch), f"G{G} d{d}")
+    args = [x.cuda() for x in (b.q, b.k, b.v, b.table, b.lens)] + [
+        torch.tensor(x, dtype=torch.int32).cuda() for x in (b.offsets, b.prefix)]
+    need = binding.attn_paged_decode_shared_workspace_size(b.S, len(b.prefix), b.Hq, b.Hkv, b.d)
+    workspaces = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    src, dst = (torch.empty(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    for i in range(40):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            dst.copy_(src)
+            dst[i::64].copy_(src[i::64])   # scattered
+            dst.copy_(src)
+        got = [binding.paged_decode_shared(*args, max_own_len=b.max_own, workspace=w) for w in workspaces]
+        for o, lse, ws in got:
+            assert binding.attn_paged_decode_check(ws)[1] == 0
+            assert torch.equal(o.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
+    torch.cuda.synchronize()
+
+
 def test_shared_large_batches(cuda):
     # thousands of sequences in more than a thousand groups (the plan's windows and searches), whose tables hold
     # whole prefixes: the ordinary decode gives the same result on the same pages

@@ -288,15 +288,24 @@ struct AttendLayout {
   // ring depths: K tiles are free once their scores are formed, V tiles only
   // after the softmax, so V gets the one that is left of 227 KB
   static constexpr int kKStages = D == 128 ? 2 : 4, kVStages = D == 128 ? 3 : 6;
+  // A tile's arrival has a barrier of its own number, from a ring longer than the
+  // slots.  A wait sees its phase's parity only, so whoever waits for tile g must
+  // know that tile g - R, the one before on that barrier, has landed; a row tile that
+  // takes every other step never waits for the steps between.  It has seen K tile
+  // g - 2 or a later one (V: g - 4, scores run ahead of the products), and copies go
+  // out in order, each after the release of the tile one slot ring before: all up to
+  // g - 2 - kKStages (g - 4 - kVStages) have landed.
+  static constexpr int kKBars = D == 128 ? 4 : 8, kVBars = D == 128 ? 8 : 16;
+  static_assert(kKBars >= kKStages + 2 && kVBars >= kVStages + 4, "a barrier's phase before has completed");
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + 2 * kTileBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
   static constexpr int kSeg = kV + kVStages * kTileBytes;
   static constexpr int kRed = kSeg + kSegments * static_cast<int>(sizeof(Segment));   // [row tile][2][4 warps][8] floats
   static constexpr int kBar = kRed + 2 * 2 * 4 * 8 * 4;
-  // k_full, k_empty, v_full, v_empty; per row tile: s_full[2], p_ready[2], o_free, o_done[2], exchange, own s_full[2], q_full[]; segment full, empty;
+  // k_full, v_full, k_empty, v_empty; per row tile: s_full[2], p_ready[2], o_free, o_done[2], exchange, own s_full[2], q_full[]; segment full, empty;
   // mma_done, windows read
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 20 + 2 * kQLoads + 2 * kSegments + 2;
+  static constexpr int kNumBars = kKBars + kVBars + kKStages + kVStages + 20 + 2 * kQLoads + 2 * kSegments + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort flag, status word; line's cost, CTA's share
   // slack to align the base to 1024 B; with d = 64 the own-keys product reads 64 rows it does not need, 1 KB on
   static constexpr int kAlloc = kMisc + 32 + 1024 + (D == 64 ? 1024 : 0);
@@ -317,12 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
-  constexpr uint32_t KS = L::kKStages, VS = L::kVStages;
-  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (2 * KS + 2 * VS), bar_s = bar_t + 8u * (20 + 2 * kQLoads);
-  auto BAR_KF = [&](uint32_t s) { return bar0 + 8u * s; };
-  auto BAR_KE = [&](uint32_t s) { return bar0 + 8u * (KS + s); };
-  auto BAR_VF = [&](uint32_t s) { return bar0 + 8u * (2 * KS + s); };
-  auto BAR_VE = [&](uint32_t s) { return bar0 + 8u * (2 * KS + VS + s); };
+  constexpr uint32_t KS = L::kKStages, VS = L::kVStages, KB = L::kKBars, VB = L::kVBars;
+  const uint32_t bar0 = sbase + L::kBar, bar_t = bar0 + 8u * (KB + VB + KS + VS), bar_s = bar_t + 8u * (20 + 2 * kQLoads);
+  auto BAR_KF = [&](uint32_t g) { return bar0 + 8u * (g % KB); };          // of tile g
+  auto BAR_VF = [&](uint32_t g) { return bar0 + 8u * (KB + g % VB); };
+  auto BAR_KE = [&](uint32_t s) { return bar0 + 8u * (KB + VB + s); };     // of slot s
+  auto BAR_VE = [&](uint32_t s) { return bar0 + 8u * (KB + VB + KS + s); };
   auto BAR_SF = [&](int t, int h) { return bar_t + 8u * (2 * t + h); };
   auto BAR_PR = [&](int t, uint32_t h) { return bar_t + 8u * (4 + 2 * t + h); };
   auto BAR_OF = [&](int t) { return bar_t + 8u * (8 + t); };
@@ -351,14 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // ---- setup
   if (threadIdx.x == 0) {
-    for (uint32_t s = 0; s < KS; ++s) {
-      mbar_init(BAR_KF(s), 1);
-      mbar_init(BAR_KE(s), 2);   // both row tiles' warps (narrow: twice by the one that takes the step)
-    }
-    for (uint32_t s = 0; s < VS; ++s) {
-      mbar_init(BAR_VF(s), 1);
-      mbar_init(BAR_VE(s), 2);
-    }
+    for (uint32_t b = 0; b < KB + VB; ++b) mbar_init(bar0 + 8u * b, 1);
+    for (uint32_t s = 0; s < KS + VS; ++s) mbar_init(BAR_KE(s), 2);   // both row tiles' warps (narrow: twice by the one that takes the step)
     for (int t = 0; t < 2; ++t) {
       for (uint32_t u = 0; u < kQLoads; ++u) mbar_init(BAR_QF(t, u), 1);
       for (int h = 0; h < 2; ++h) {
@@ -615,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per_tile = kTile / a.page_size;
       const uint32_t page_bytes = static_cast<uint32_t>(a.page_size) * D * 2;
       const uint32_t stages = is_v ? VS : KS, data = is_v ? sV : sK;
-      const uint32_t full0 = is_v ? BAR_VF(0) : BAR_KF(0), empty0 = is_v ? BAR_VE(0) : BAR_KE(0);
+      const uint32_t full0 = is_v ? BAR_VF(0) : BAR_KF(0), bars = is_v ? VB : KB, empty0 = is_v ? BAR_VE(0) : BAR_KE(0);
       const CUtensorMap* tm = is_v ? &tmV : &tmK;
-      uint32_t slot = 0, use = 0;   // ring slot of the next tile, and how often the ring went round
+      uint32_t slot = 0, use = 0, g = 0;   // ring slot of the next tile, how often the ring went round, tiles copied
       uint32_t qn[2] = {0, 0};      // loads into each query buffer
       uint32_t qlast[2] = {0, 0};   // ring position of the last step that reads each
       bool qown[2] = {false, false};
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = j + 1 < tiles && lane < per_tile && static_cast<long long>(p) * a.page_size < hi;
           if (more) pg_next = __ldg(row + p);
           if (!(ok = wait_all(empty0 + 8u * slot, (use & 1u) ^ 1u, status, abort_flag))) break;
-          const uint32_t bar = full0 + 8u * slot;
+          const uint32_t bar = full0 + 8u * (g % bars);
           const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(live)) * page_bytes);
           __syncwarp();
@@ -681,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t at = data + slot * L::kTileBytes + static_cast<uint32_t>(lane) * page_bytes;
             tma_load_5d(at, tm, bar, 0, 0, 0, is_v ? hkv : 0, is_v ? pg : pg * a.Hkv + hkv);
           }
+          ++g;
           if (++slot == stages) {
             slot = 0;
             ++use;
@@ -700,9 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t u = qn[t] > kQLoads ? qn[t] - kQLoads : 0u; u < qn[t]; ++u)
             mbar_wait(BAR_QF(t, u), (u / kQLoads) & 1u, nullptr, nullptr, kWaitLimitNs);
 #pragma unroll 1
-        for (uint32_t k = 0; k < stages; ++k)   // the last fill of each slot
-          if (use > 0 || k < slot)
-            mbar_wait(full0 + 8u * k, (k < slot ? use : use - 1) & 1u, nullptr, nullptr, kWaitLimitNs);
+        for (uint32_t k = g > stages ? g - stages : 0u; k < g; ++k)   // the last fill of each slot
+          mbar_wait(full0 + 8u * (k % bars), (k / bars) & 1u, nullptr, nullptr, kWaitLimitNs);
       }
       __syncwarp();
     } else {
@@ -764,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t g = gs + static_cast<uint32_t>(j);
             if (have) {
               const uint32_t ks = g % KS;
-              if (!(ok = wait_all(BAR_KF(ks), (g / KS) & 1u, status, abort_flag))) break;
+              if (!(ok = wait_all(BAR_KF(g), (g / KB) & 1u, status, abort_flag))) break;
               tc_fence_after();
               if (leader) {
                 const uint64_t a0 = dK + ks * kTileStep;
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (k > 0) {   // the product of the step before, by now the softmax may be a step further: two barriers in turn
               const uint32_t vs = pg % VS;
-              if (!(ok = wait_all(BAR_VF(vs), (pg / VS) & 1u, status, abort_flag))) break;
+              if (!(ok = wait_all(BAR_VF(pg), (pg / VB) & 1u, status, abort_flag))) break;
               if (pfirst && pused > 0 && !(ok = wait_all(BAR_OF(t), (pused - 1) & 1u, status, abort_flag))) break;
               if (!(ok = wait_all(BAR_PR(t, (k - 1) & 1u), (steps_t + ((k - 1) >> 1)) & 1u, status, abort_flag))) break;
               tc_fence_after();
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = j + stride < tiles;
           const uint32_t g = gs - static_cast<uint32_t>(stride), vs = g % VS;
           q = 0;
-          if (j >= 0 && !(ok = wait_all(BAR_VF(vs), (g / VS) & 1u, status, abort_flag))) break;
+          if (j >= 0 && !(ok = wait_all(BAR_VF(g), (g / VB) & 1u, status, abort_flag))) break;
           // the first product of a segment overwrites O_t: the epilogue before must have read it
           if (j == first && used > 0 && !(ok = wait_all(BAR_OF(t), (used - 1) & 1u, status, abort_flag))) break;
 #pragma unroll 1
@@ -876,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait_all(BAR_OD(t, h), steps_t & 1u, status, abort_flag))) break;
             }
             // the next step's scores: of this half if K is there, else both later
-            const uint32_t kf = BAR_KF(gs % KS), kph = (gs / KS) & 1u;
+            const uint32_t kf = BAR_KF(gs), kph = (gs / KB) & 1u;
             if (more && (h == 1 || __all_sync(0xffffffffu, mbar_try_wait(kf, kph)))) {
               if (!(ok = wait_all(kf, kph, status, abort_flag))) break;
               tc_fence_after();
@@ -945,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both row tiles' warps, each before its own product).
       auto zero_values = [&](int j, int lo, int lim) {
         const uint32_t gj = sg.g0 + static_cast<uint32_t>(j), sv = gj % VS;
-        if (!wait_all(BAR_VF(sv), (gj / VS) & 1u, status, abort_flag)) return false;
+        if (!wait_all(BAR_VF(gj), (gj / VB) & 1u, status, abort_flag)) return false;
         if (lane_row >= lim || lane_row < lo) {
           const int pr = lane_row & (a.page_size - 1);
           uint8_t* base = smem + L::kV + sv * L::kTileBytes + (lane_row - pr) * D * 2 + pr * 128;
