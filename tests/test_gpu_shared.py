@@ -377,6 +377,11 @@ def test_shared_refusals(cuda):
                    (1, args[1].transpose(1, 2))):
         with pytest.raises(ValueError):
             binding.paged_decode_shared(*args[:i], bad, *args[i + 1:])
+    for over in (dict(out=args[0].float()), dict(out=args[0][:1]), dict(lse=torch.empty(1, 4, device="cuda")),
+                 dict(lse=torch.empty(2, 4, dtype=torch.bfloat16, device="cuda")),
+                 dict(workspace=torch.empty(1 << 26, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            binding.paged_decode_shared(*args, **over)
     with pytest.raises(binding.TiledAttnError):
         binding.paged_decode_shared(*args, workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
     with pytest.raises(binding.TiledAttnError):

@@ -577,6 +577,13 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
     _ints("seq_lens", seq_lens, (S,), dev)
     _ints("group_offsets", group_offsets, (groups + 1,), dev)
     _ints("prefix_lens", prefix_lens, (groups,), dev)
+    if out is not None and (not _rows("out", out, (S, Hq, d)).is_contiguous() or out.device != dev):
+        raise ValueError(f"out must be contiguous and on {dev}")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (S, Hq) or lse.device != dev
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor {(S, Hq)} on {dev}")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous and on {dev}")
     if max_own_len is None:
         max_own_len = max_pages * ps
     if scale is None:
