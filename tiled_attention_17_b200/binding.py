@@ -402,27 +402,22 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     return o, lse, workspace
 
 
-class _Here:
-    """No change of device or stream (cheaper than contextlib.nullcontext, made once)."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
+def _here(device):
+    """The handle of the current stream if `device` is the current device, else None.  (The calls below are a few
+    microseconds of kernel in their small sizes, so a Stream object, 3 us, or a device guard is too much.)"""
+    import torch
+    raw, current = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw and current:
+        return raw(device.index) if current() == device.index else None
+    return torch.cuda.current_stream().cuda_stream if torch.cuda.current_device() == device.index else None
 
 
 def _scope(device, stream):
     """The device and stream a convenience call allocates and launches on: the
     tensors' device, and `stream` (a torch stream or its handle) or that
     device's current one.  What the call allocates belongs to that stream."""
-    import torch
-    if stream is None and device.index == torch.cuda.current_device():
-        return _HERE
     import contextlib
+    import torch
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -435,7 +430,7 @@ def _scope(device, stream):
 def _rows(name, t, shape=None):
     """A bf16 CUDA tensor whose last dimension is contiguous."""
     import torch
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be a bf16 CUDA tensor with contiguous rows")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -466,7 +461,8 @@ def _rope(x, inv_freq, positions, interleaved, amplitude, out, stream, inverse):
     if x.dim() != 4:
         raise ValueError(f"x must be [B, H, N, d], got {tuple(x.shape)}")
     B, H, N, d = x.shape
-    _rows("x", x)
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.stride(3) != 1:
+        _rows("x", x)
     device = x.device
     rotary_dim = _frequencies(inv_freq, device)
     pos_stride = 0
@@ -478,13 +474,20 @@ def _rope(x, inv_freq, positions, interleaved, amplitude, out, stream, inverse):
             pos_stride = N
     if out is not None and _rows("out", out, x.shape).device != device:
         raise ValueError("out must be on x's device")
-    with _scope(device, stream):
-        if out is None:
-            out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
-        xb, xh, xn, _ = x.stride()
-        yb, yh, yn, _ = out.stride()
-        attn_rope(x, out, positions, inv_freq, B, H, N, d, rotary_dim, interleaved, inverse, amplitude,
-                  xb, xh, xn, yb, yh, yn, pos_stride)
+    handle = _here(device) if stream is None else None
+    if handle is None:
+        with _scope(device, stream):
+            return _rope(x, inv_freq, positions, interleaved, amplitude, out, None, inverse)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    xb, xh, xn, _ = x.stride()
+    yb, yh, yn, _ = out.stride()
+    code = (_lib or load()).attn_rope(
+        x.data_ptr(), out.data_ptr(), None if positions is None else positions.data_ptr(),
+        None if inv_freq is None else inv_freq.data_ptr(), B, H, N, d, rotary_dim, int(interleaved), inverse,
+        float(amplitude), xb, xh, xn, yb, yh, yn, pos_stride, handle)
+    if code:
+        _check("attn_rope", code)
     return out
 
 
@@ -521,7 +524,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None,
     S, max_pages = block_table.shape
     dev = k.device
     _rows("k", k)
-    _rows("v", v, k.shape)
+    _rows("v", v, (T, Hkv, d))
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not _rows(name, t, (P, Hkv, ps, d)).is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -532,24 +535,37 @@ def paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None,
     if positions is not None:
         _ints("positions", positions, (T,), dev)
     rotary_dim = _frequencies(inv_freq, dev)
-    Hq, qs = 0, (0, 0)
-    if q is not None:
+    Hq, qt, qh = 0, 0, 0
+    if q is None:
+        q_out = None
+    else:
         Hq = q.shape[1]
         _rows("q", q, (T, Hq, d))
-        qs = q.stride()
-    if any(t is not None and t.device != dev for t in (v, k_cache, v_cache, q, q_out)):
-        raise ValueError("all tensors must be on one device")
-    with _scope(dev, stream):
-        if q is None:
-            q_out = None
-        elif q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-        elif not _rows("q_out", q_out, (T, Hq, d)).is_contiguous():
+        qt, qh, _ = q.stride()
+        if q_out is not None and not _rows("q_out", q_out, (T, Hq, d)).is_contiguous():
             raise ValueError("q_out must be contiguous")
-        ks, vs = k.stride(), v.stride()
-        attn_paged_append(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, seq_lens, positions, inv_freq,
-                          ps, S, T, Hq, Hkv, d, max_pages, P, rotary_dim, interleaved, amplitude, qs[0], qs[1],
-                          ks[0], ks[1], vs[0], vs[1])
+    here = k.get_device()
+    if here != v.get_device() or here != k_cache.get_device() or here != v_cache.get_device() \
+            or q is not None and here != q.get_device() or q_out is not None and here != q_out.get_device():
+        raise ValueError("all tensors must be on one device")
+    handle = _here(dev) if stream is None else None
+    if handle is None:
+        with _scope(dev, stream):
+            return paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens, q, q_out, inv_freq, positions,
+                                interleaved, amplitude)
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    code = (_lib or load()).attn_paged_append(
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), None if q is None else q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+        None if positions is None else positions.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
+        ps, S, T, Hq, Hkv, d, max_pages, P, rotary_dim, int(interleaved), float(amplitude), qt, qh, kt, kh, vt, vh,
+        handle)
+    if code:
+        _check("attn_paged_append", code)
     return q_out
 
 
@@ -588,15 +604,23 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
         max_own_len = max_pages * ps
     if scale is None:
         scale = d ** -0.5
-    with _scope(dev, stream):
-        if workspace is None:
-            need = attn_paged_decode_shared_workspace_size(S, groups, Hq, Hkv, d)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
-        attn_paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, ps, S, groups,
-                                 max_own_len, Hq, Hkv, d, max_pages, P, scale, out, lse, workspace,
-                                 workspace.numel() * workspace.element_size())
+    handle = _here(dev) if stream is None else None
+    if handle is None:
+        with _scope(dev, stream):
+            return paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens,
+                                       max_own_len, scale, workspace, out, lse)
+    if workspace is None:
+        need = attn_paged_decode_shared_workspace_size(S, groups, Hq, Hkv, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = q.new_empty((S, Hq), dtype=torch.float32)
+    code = (_lib or load()).attn_paged_decode_shared(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        group_offsets.data_ptr(), prefix_lens.data_ptr(), ps, S, groups, max_own_len, Hq, Hkv, d, max_pages, P,
+        float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), handle)
+    if code:
+        _check("attn_paged_decode_shared", code)
     return out, lse, workspace
