@@ -57,6 +57,7 @@ constexpr float kRescaleLog2 = 8.0f;   // the stale-max margin of the prefill ke
 // partial is 128 KB, and the pipeline starts again): without a cost of its own the
 // CTAs with two of them ended 25% after the median of a small batch.
 constexpr int kWideCost = 5, kNarrowCost = 3, kWideStart = 8;
+constexpr int kApart = 1000;   // cycles between the row tiles' first softmax of a wide segment
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -713,14 +714,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Each tile's chain - scores, softmax, product with V, next scores - is a
       // string of waits and issues of some hundred cycles each; from one warp the
       // two tiles' chains add up (a narrow step took 2.4 us), from two they overlap.
-      const int t = warp == kMmaWarp1 ? 1 : 0;
+      const int t = __shfl_sync(0xffffffffu, warp == kMmaWarp1 ? 1 : 0, 0);
       const bool leader = elect_one_sync();
       constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile / 2, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kTile, D, true);
-      const uint32_t tS = tmem + (t ? L::kTmS1 : L::kTmS0), tO = tmem + (t ? L::kTmO1 : L::kTmO0);
+      const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t tS = tbase + (t ? L::kTmS1 : L::kTmS0), tO = tbase + (t ? L::kTmO1 : L::kTmO0);
       constexpr bool kTwo = L::kChunks == 2;
       constexpr uint64_t kTileStep = L::kTileBytes >> 4;
-      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024) + t * kTileStep;
+      // (made from the tile's address: adding t tiles to a descriptor, with t the same in all lanes, came out of the
+      // compiler with a wrong upper half, and every row but a tile's first was wrong)
+      const uint64_t dQ = smem_desc_sw128(sQ + (t ? L::kTileBytes : 0), 16, 1024);
       const uint64_t dK = smem_desc_sw128(sK, 16, L::kChunks * 1024);   // 8-row groups hold every chunk
       const int ps = a.page_size;
       const uint64_t dV = kTwo ? smem_desc_sw128(sV, static_cast<uint32_t>(ps) * 128u, ps >= 16 ? 1024u : 2048u)
@@ -879,12 +883,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait_all(BAR_OD(t, h), steps_t & 1u, status, abort_flag))) break;
             }
             // the next step's scores: of this half if K is there, else both later
-            const uint32_t kf = BAR_KF(gs), kph = (gs / KB) & 1u;
-            if (more && (h == 1 || __all_sync(0xffffffffu, mbar_try_wait(kf, kph)))) {
-              if (!(ok = wait_all(kf, kph, status, abort_flag))) break;
-              tc_fence_after();
+            if (more) {
+              const uint32_t kf = BAR_KF(gs), kph = (gs / KB) & 1u;
+              bool there = q > 0;   // known since the half before
+              if (!there)
+                there = h == 0 ? __all_sync(0xffffffffu, mbar_try_wait(kf, kph)) : (ok = wait_all(kf, kph, status, abort_flag));
+              if (!ok) break;
+              if (there) {
+                tc_fence_after();
 #pragma unroll 1
-              for (; q <= h; ++q) scores(gs, q);
+                for (; q <= h; ++q) scores(gs, q);
+              }
             }
           }
           if (!ok) break;
@@ -1093,6 +1102,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h, first = false) {   // 64 keys
           ok = wait_all(BAR_SF(t, h), steps_t & 1u, status, abort_flag);
           if (!ok) break;
+          // Two row tiles in step form their exponentials at the same time (985 cycles for 64 of them, twice one warp's
+          // time) and leave the unit idle at the same time.  Nothing moves them apart, so tile 1 starts a segment a
+          // quarter of a step late: 256 samples behind 30000 tokens 164 -> 162 us, 64 behind 8000 tokens 45.0 -> 43.7
+          // (700 cycles: 167 and 43.7).
+          if (t == 1 && first && sg.wide)
+            for (const long long t0 = clock64(); clock64() - t0 < kApart;) {
+            }
           tc_fence_after();
           ++(h ? held1 : held0);   // this half's product is a phase of its barrier
           if (need_mask && h == 0) {
