@@ -9,13 +9,20 @@
 // a matrix product: rows are (sequence, query head of one KV head) pairs, 128
 // to a tile, and a K/V tile of 128 keys is read once for up to 256 rows.
 //
-// Own keys run through the same tiles with Hq / Hkv rows of the 128 in use.
-// The waste is free: a 128-key tile of K and V is 64 KB, 1.5 us of one SM's
-// share of HBM, and its two products take 0.6 us of the tensor pipe however
-// many rows count, while the CUDA-core dot products of the paged decode are
-// bound by instructions at such short lengths (48 us here against 10 us of
-// bytes for 64 sequences of about 256 own tokens, 104 us against 8 us with
-// groups of 8 heads at d = 64).
+// Own keys go through the tensor cores too, with the products transposed (S^T =
+// K Q^T, O^T = V^T P^T: keys, then columns of d, on the 128 rows and 16 columns of
+// queries).  The dot products of the paged decode are bound by instructions at
+// such short lengths: 48 us against 10 us of bytes for 64 sequences of about 256
+// own tokens, 104 us against 8 us with groups of 8 heads at d = 64.
+//
+// Measured (B200, whole call, L2 cold): 64 sequences, 32 + 8 heads of 128, 8000
+// shared and up to 512 own tokens 42 us (the bytes alone 15); 96 sequences in 6
+// groups, 32 + 4 heads of 64, 5000 shared and up to 1024 own tokens 45 us (12);
+// 256 sequences behind 30000 tokens 163 us (products 77: 780 TFLOP/s).  The time
+// goes to the start (6 us: plan, tensor memory, first tiles), the steps, and the
+// join (7 us).  A step with two row tiles, 128 keys, takes 3800 cycles, of which
+// tensor pipe 2600 (products of 64 keys are bound by the reads of Q from shared
+// memory) and exponentials 2050: neither role waits for the other any more.
 //
 // Two kernels, the second a programmatic dependent of the first:
 //   shared_attend_kernel   all products, cut evenly over the SMs
@@ -263,7 +270,8 @@ struct __align__(16) Segment {
   int slot;        // of its partials: >= 0 prefix, ~slot own keys
   int hkv, seq;    // KV head, first sequence of the query rows
   int row, page0;  // block-table row, its first page
-  int qslot, pad[3];      // own keys: where in the query buffers its rows are (in 8 rows)
+  int qslot;       // own keys: where in the query buffers its rows are (in 8 rows)
+  int pad[3];
   int pages[kTile / 8];   // physical pages of its first key tile, -1 past the keys
 };
 static_assert(sizeof(Segment) == 128, "16-byte loads");
@@ -1230,9 +1238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Combine: one CTA per (KV head, sequence), thread (c4, g) joins the partials of
-// columns [4 c4, 4 c4 + 4) of query head g.  Weights e^(lse_i - max) over all
-// partials of a row.  No shared memory and few registers, so its first CTAs wait
-// on the SMs beside the attend kernel's.
+// columns [4 c4, 4 c4 + 4) of query head g, with kLanes = 2 two threads half of
+// them each.  Weights e^(lse_i - max) over all partials of a row.  Bound by
+// latency: the release of the first grid, two dependent loads of the plan and one
+// round of partials from L2, 7 us after the last attend CTA for 64 sequences of 32
+// heads.  (16 partials in flight a thread instead of 8 were as good at small
+// batches and 2% slower at 256 sequences.)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ long long divide(long long x, long long y) {   // both >= 0; in 32 bits where it fits
   return ((x | y) >> 32) == 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(y) : x / y;
@@ -1244,9 +1255,10 @@ __device__ __forceinline__ void unit_ctas(long long x0, int tiles, int cost, lon
   n = static_cast<int>(divide(x0 + static_cast<long long>(tiles - 1) * cost, per)) - c0 + 1;
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedArgs a, __nv_bfloat16* o, float* lse) {
-  const int hkv = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, c4 = tid / G, gq = tid % G;
+template <int D, int G, int kLanes>
+__global__ void __launch_bounds__(G * D / 4 * kLanes) shared_combine_kernel(const SharedArgs a, __nv_bfloat16* o, float* lse) {
+  const int hkv = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x / kLanes, lane0 = threadIdx.x % kLanes;
+  const int c4 = tid / G, gq = tid % G;
   grid_wait();   // the partials are complete
   const SeqPlan sp = a.seqs[seq];
   const long long per = *a.per_cta;
@@ -1285,17 +1297,17 @@ __global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedA
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kAhead = 8;   // partials loaded before the first is joined
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
+  for (int i0 = lane0; i0 < n; i0 += kAhead * kLanes) {
     float w[kAhead];
     float4 v[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       w[k] = -INFINITY;
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + k < n) {
+      if (i0 + k * kLanes < n) {
         const float* pw;
         const float4* pv;
-        place(i0 + k, pw, pv);
+        place(i0 + k * kLanes, pw, pv);
         w[k] = *pw;
         v[k] = *pv;
       }
@@ -1319,13 +1331,26 @@ __global__ void __launch_bounds__(G * D / 4) shared_combine_kernel(const SharedA
         acc.w = fmaf(s1, v[k].w, acc.w);
       }
   }
-  constexpr int kGather = G * D / 4 < 32 ? G * D / 4 : 32;
-  if (hkv == 0 && seq == 0 && tid < kGather) {   // the call's status: any CTA's
-    unsigned bits = 0;
-    for (int c = tid; c < a.n_ctas; c += kGather) bits |= a.cta_status[c];
-    bits = __reduce_or_sync(kGather == 32 ? 0xffffffffu : (1u << kGather) - 1u, bits);
-    if (tid == 0) *a.status = bits;
+  if constexpr (kLanes == 2) {   // the other lane's partials (the block is whole warps)
+    const float m1 = __shfl_xor_sync(0xffffffffu, m, 1), l1 = __shfl_xor_sync(0xffffffffu, l, 1), mn = fmaxf(m, m1);
+    const float s0 = m == -INFINITY ? 0.f : __expf(m - mn), s1 = m1 == -INFINITY ? 0.f : __expf(m1 - mn);
+    // both lanes the same sums, term for term
+    const float t0 = l * s0, t1 = l1 * s1;
+    l = t0 + t1;
+    acc.x = acc.x * s0 + __shfl_xor_sync(0xffffffffu, acc.x * s0, 1);
+    acc.y = acc.y * s0 + __shfl_xor_sync(0xffffffffu, acc.y * s0, 1);
+    acc.z = acc.z * s0 + __shfl_xor_sync(0xffffffffu, acc.z * s0, 1);
+    acc.w = acc.w * s0 + __shfl_xor_sync(0xffffffffu, acc.w * s0, 1);
+    m = mn;
   }
+  constexpr int kThreadsHere = G * D / 4 * kLanes, kGather = kThreadsHere < 32 ? kThreadsHere : 32;
+  if (hkv == 0 && seq == 0 && threadIdx.x < kGather) {   // the call's status: any CTA's
+    unsigned bits = 0;
+    for (int c = threadIdx.x; c < a.n_ctas; c += kGather) bits |= a.cta_status[c];
+    bits = __reduce_or_sync(kGather == 32 ? 0xffffffffu : (1u << kGather) - 1u, bits);
+    if (threadIdx.x == 0) *a.status = bits;
+  }
+  if (lane0 != 0) return;
   const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
   const size_t orow = static_cast<size_t>(seq) * a.Hq + hkv * G + gq;
   uint2 w2;
@@ -1392,14 +1417,24 @@ ta_status launch_attend(const void* q, const void* k_cache, const void* v_cache,
   return e == cudaSuccess ? TA_OK : fail(TA_ERR_CUDA, "shared decode: attend kernel launch", e);
 }
 
+template <int D, int G>
+cudaError_t launch_combine_of(const SharedArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.num_seqs));
+  constexpr int kBlock = G * D / 4;
+  // Two lanes an output, each with half of the partials, as long as all of them run at once (2048 threads an SM):
+  // 64 sequences of 32 heads 43.9 -> 42.2 us for the whole call, 96 of 32 heads 47.1 -> 45.4.  Beyond that a second
+  // wave costs more than the shorter loop gives (256 of 32 heads: 163.6 with one lane, 167.3 with two).
+  if (static_cast<long long>(a.Hkv) * a.num_seqs * (2 * kBlock) <= a.n_ctas * 2048ll)
+    return launch(shared_combine_kernel<D, G, 2>, grid, 2 * kBlock, 0, true, stream, a, o, lse);
+  return launch(shared_combine_kernel<D, G, 1>, grid, kBlock, 0, true, stream, a, o, lse);
+}
 template <int D>
 cudaError_t launch_combine(const SharedArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.num_seqs));
   switch (a.G) {
-    case 1: return launch(shared_combine_kernel<D, 1>, grid, 1 * D / 4, 0, true, stream, a, o, lse);
-    case 2: return launch(shared_combine_kernel<D, 2>, grid, 2 * D / 4, 0, true, stream, a, o, lse);
-    case 4: return launch(shared_combine_kernel<D, 4>, grid, 4 * D / 4, 0, true, stream, a, o, lse);
-    default: return launch(shared_combine_kernel<D, 8>, grid, 8 * D / 4, 0, true, stream, a, o, lse);
+    case 1: return launch_combine_of<D, 1>(a, o, lse, stream);
+    case 2: return launch_combine_of<D, 2>(a, o, lse, stream);
+    case 4: return launch_combine_of<D, 4>(a, o, lse, stream);
+    default: return launch_combine_of<D, 8>(a, o, lse, stream);
   }
 }
 
