@@ -55,3 +55,11 @@ def test_shared_workspace_size(lib):
     assert size(65536, 1, 32, 8, 128) == 0
     assert size(64, 65536, 32, 8, 128) == 0
     assert size(64, -1, 32, 8, 128) == 0
+
+
+def test_stream_of_another_device_is_refused():
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    from tiled_attention_17_b200 import binding
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        binding._scope(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)))

@@ -418,11 +418,14 @@ def _scope(device, stream):
     device's current one.  What the call allocates belongs to that stream."""
     import contextlib
     import torch
-    stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.device(device))
     if stream is not None:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
         stack.enter_context(torch.cuda.stream(stream))
     return stack
 
