@@ -402,14 +402,20 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     return o, lse, workspace
 
 
+_raw_stream = _raw_device = None
+
+
 def _here(device):
     """The handle of the current stream if `device` is the current device, else None.  (The calls below are a few
     microseconds of kernel in their small sizes, so a Stream object, 3 us, or a device guard is too much.)"""
-    import torch
-    raw, current = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-    if raw and current:
-        return raw(device.index) if current() == device.index else None
-    return torch.cuda.current_stream().cuda_stream if torch.cuda.current_device() == device.index else None
+    global _raw_stream, _raw_device
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    index = device.index
+    return _raw_stream(index) if _raw_device() == index else None
 
 
 def _scope(device, stream):
@@ -442,7 +448,7 @@ def _rows(name, t, shape=None):
 
 def _ints(name, t, shape, device):
     import torch
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t
@@ -526,18 +532,26 @@ def paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None,
     P, _, ps, _ = k_cache.shape
     S, max_pages = block_table.shape
     dev = k.device
-    _rows("k", k)
-    _rows("v", v, (T, Hkv, d))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not _rows(name, t, (P, Hkv, ps, d)).is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    rows, pool = k.shape, k_cache.shape
+    rotary_dim = _frequencies(inv_freq, dev)
+    bf16, i32, index = torch.bfloat16, torch.int32, k.get_device()
+    if (k.dtype is not bf16 or v.dtype is not bf16 or k_cache.dtype is not bf16 or v_cache.dtype is not bf16
+            or v.shape != rows or pool != (P, Hkv, ps, d) or v_cache.shape != pool or index < 0
+            or v.get_device() != index or k_cache.get_device() != index or v_cache.get_device() != index
+            or k.stride(2) != 1 or v.stride(2) != 1 or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        _rows("k", k)
+        _rows("v", v, rows)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if not _rows(name, t, (P, Hkv, ps, d)).is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if not index == v.get_device() == k_cache.get_device() == v_cache.get_device():
+            raise ValueError("all tensors must be on one device")
     _ints("block_table", block_table, (S, max_pages), dev)
     _ints("seq_lens", seq_lens, (S,), dev)
     if cu_seqlens is not None:
         _ints("cu_seqlens", cu_seqlens, (S + 1,), dev)
     if positions is not None:
         _ints("positions", positions, (T,), dev)
-    rotary_dim = _frequencies(inv_freq, dev)
     Hq, qt, qh = 0, 0, 0
     if q is None:
         q_out = None
@@ -547,10 +561,8 @@ def paged_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None,
         qt, qh, _ = q.stride()
         if q_out is not None and not _rows("q_out", q_out, (T, Hq, d)).is_contiguous():
             raise ValueError("q_out must be contiguous")
-    here = k.get_device()
-    if here != v.get_device() or here != k_cache.get_device() or here != v_cache.get_device() \
-            or q is not None and here != q.get_device() or q_out is not None and here != q_out.get_device():
-        raise ValueError("all tensors must be on one device")
+        if q.get_device() != index or q_out is not None and q_out.get_device() != index:
+            raise ValueError("all tensors must be on one device")
     handle = _here(dev) if stream is None else None
     if handle is None:
         with _scope(dev, stream):
@@ -588,10 +600,14 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
     max_pages = block_table.shape[1]
     groups = prefix_lens.shape[0]
     dev = q.device
-    for name, t, shape in (("q", q, (S, Hq, d)), ("k_cache", k_cache, (P, Hkv, ps, d)),
-                           ("v_cache", v_cache, (P, Hkv, ps, d))):
-        if not _rows(name, t, shape).is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be contiguous and on {dev}")
+    bf16, index, pool = torch.bfloat16, q.get_device(), k_cache.shape
+    if (q.dtype is not bf16 or k_cache.dtype is not bf16 or v_cache.dtype is not bf16 or pool[3] != d
+            or v_cache.shape != pool or index < 0 or k_cache.get_device() != index or v_cache.get_device() != index
+            or not q.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        for name, t, shape in (("q", q, (S, Hq, d)), ("k_cache", k_cache, (P, Hkv, ps, d)),
+                               ("v_cache", v_cache, (P, Hkv, ps, d))):
+            if not _rows(name, t, shape).is_contiguous() or t.device != dev:
+                raise ValueError(f"{name} must be contiguous and on {dev}")
     _ints("block_table", block_table, (S, max_pages), dev)
     _ints("seq_lens", seq_lens, (S,), dev)
     _ints("group_offsets", group_offsets, (groups + 1,), dev)
@@ -614,7 +630,7 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_offset
                                        max_own_len, scale, workspace, out, lse)
     if workspace is None:
         need = attn_paged_decode_shared_workspace_size(S, groups, Hq, Hkv, d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
