@@ -18,7 +18,7 @@
 // Measured (B200, whole call, L2 cold): 64 sequences, 32 + 8 heads of 128, 8000
 // shared and up to 512 own tokens 42 us (the bytes alone 15); 96 sequences in 6
 // groups, 32 + 4 heads of 64, 5000 shared and up to 1024 own tokens 45 us (12);
-// 256 sequences behind 30000 tokens 163 us (products 77: 780 TFLOP/s).  The time
+// 256 sequences behind 30000 tokens 162 us, 190 in a long run (products 77).  The time
 // goes to the start (6 us: plan, tensor memory, first tiles), the steps, and the
 // join (7 us).  A step with two row tiles, 128 keys, takes 3800 cycles, of which
 // tensor pipe 2600 (products of 64 keys are bound by the reads of Q from shared

@@ -12,14 +12,17 @@
 // a token leaves 0.06 rad of error in fp32): p * inv_freq / (2 pi) is formed in
 // fp64, whole turns are dropped there, and only the fraction of a turn goes to
 // fp32.  Sine and cosine of at most half a turn then come from the hardware's
-// approximation: within 2^-21 of 1, next to the 2^-9 a bf16 result is rounded by.
+// approximation: within 2^-21 of 1, next to the 2^-8 a bf16 result is rounded by.
 //
 // Bound: HBM bytes, each element read once and written once.  One thread owns
 // 16 elements (8 pairs) of a row and walks over heads of its token with the
 // eight cosines and sines in registers, so the trigonometry is paid once per
 // token and not once per head; two 16-byte loads per head, four heads in
 // flight before the first is used.  How many heads a thread walks over is
-// chosen in heads_per_thread (below).
+// chosen in heads_per_thread (below).  Measured (B200): 4 x 4096 tokens, 16 heads
+// of 128 in 24 us (5.6 TB/s), 16686 tokens of 48 rows of 128 appended in 69 us (5.9
+// TB/s), one token in 3.4 us.  With 2 or 8 heads in flight, blocks of 256, or
+// loads marked as streaming the appends take 2 to 20% longer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
