@@ -145,7 +145,8 @@ struct SharedArgs {
   const int32_t* seq_lens;
   const int32_t* group_offsets;
   const int32_t* prefix_lens;
-  int page_size, num_seqs, num_groups, Hq, Hkv, G, max_pages, num_pages_total, n_ctas, max_own;
+  int page_size, page_shift, g_shift;   // page_size = 1 << page_shift, G = 1 << g_shift
+  int num_seqs, num_groups, Hq, Hkv, G, max_pages, num_pages_total, n_ctas, max_own;
   float scale, scale_log2;
   // workspace
   unsigned* status;       // the call's status word (written by the combine kernel)
@@ -203,7 +204,9 @@ __device__ __forceinline__ Item describe_item(const SharedArgs& a, int groups, i
 
 // 32 items, one a lane, with their costs and places: base and base_u are those of
 // the first; moved on to the next 32.  (Out of line: called from three places,
-// none of them hot.)
+// none of them hot.  A CTA's first call takes 2.5 us, L2 cold or warm: the loads are
+// a few dependent ones, most of it is the first fetch of the instructions, so the
+// plan divides by shifts and products.)
 struct Window {
   Item it;
   long long cost;
@@ -214,7 +217,7 @@ __device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int 
   Window r;
   r.it = describe_item(a, groups, i, bad);
   if (r.it.end > r.it.base)   // its first pages' table entries, soon wanted by the CTA that starts there
-    prefetch_l2(a.block_table + static_cast<size_t>(r.it.first) * a.max_pages + r.it.base / a.page_size);
+    prefetch_l2(a.block_table + static_cast<size_t>(r.it.first) * a.max_pages + (r.it.base >> a.page_shift));
   const int tiles = tiles_of(r.it.end - r.it.base);
   const int units = tiles > 0 ? blocks_of(r.it.n, a.G) * a.Hkv : 0, own_units = i < groups ? units : 0;
   r.cost = units * unit_cost(tiles, cost_of(r.it.n, a.G));
@@ -236,10 +239,12 @@ __device__ __noinline__ Window load_window(const SharedArgs& a, int groups, int 
   return r;
 }
 
-// x / cost rounded up, x >= 0 (divisions by constants).
+// x / cost rounded up, x >= 0: the high half of a product with 2^66 / 5 or 2^65 / 3 rounded up, exact for 64 bits.
+static_assert(kWideCost == 5 && kNarrowCost == 3, "the reciprocals below");
 __device__ __forceinline__ long long steps_in(long long x, int cost) {
-  const unsigned long long u = static_cast<unsigned long long>(x);
-  return static_cast<long long>(cost == kWideCost ? (u + (kWideCost - 1)) / kWideCost : (u + (kNarrowCost - 1)) / kNarrowCost);
+  const unsigned long long u = static_cast<unsigned long long>(x) + static_cast<unsigned>(cost - 1);
+  const bool wide = cost == kWideCost;
+  return static_cast<long long>(__umul64hi(u, wide ? 0xCCCCCCCCCCCCCCCDull : 0xAAAAAAAAAAAAAAABull) >> (wide ? 2 : 1));
 }
 // Steps of a unit that start in CTA c's share (which reaches into the unit):
 // [j0, j1) of `tiles`, x0 the unit's place on the line, `cost` a step's.  None
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ======================= planner: describes the CTA's segments, up to kSegments ahead =======================
       const long long begin = per * blockIdx.x, end = min(line[0], begin + per);
-      const int per_tile = kTile / a.page_size;
+      const int per_tile = kTile >> a.page_shift;
       // where the walk is: window of items (one a lane, `work` those left in it), item, unit of it and the unit's place
       int w = 0, base_u = 0;
       long long base = 0;
@@ -576,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment sg = {};
         int pg = -1;
         if (!done) {
-          const int row0 = unit % blocks * kUnitRows;
+          const int head = blocks == 1 ? unit : static_cast<int>(static_cast<unsigned>(unit) / static_cast<unsigned>(blocks));
+          const int row0 = (unit - head * blocks) * kUnitRows;
           const bool is_own = own;   // advance() moves on
           sg.g0 = g0;
           sg.tiles = j1 - j0;
@@ -587,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           sg.hi = it.end - it.base - j0 * kTile;
           const int slot = static_cast<int>(blockIdx.x) + it.unit0 + unit;
           sg.slot = is_own ? ~slot : slot;
-          sg.hkv = unit / blocks;
-          sg.seq = it.first + row0 / a.G;
+          sg.hkv = head;
+          sg.seq = it.first + (row0 >> a.g_shift);
           sg.row = it.first;
-          sg.page0 = it.base / a.page_size + j0 * per_tile;
+          sg.page0 = (it.base >> a.page_shift) + j0 * per_tile;
           sg.qslot = is_own ? static_cast<int>(n % kQSlots) : 0;
           g0 += sg.tiles;
           if (!sg.wide) turn ^= sg.tiles & 1;
@@ -624,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2 || warp == 3) {
       // ======================= copying warps: 2 queries and K, 3 V (lane p: page p of a key tile) =======================
       const bool is_v = warp == 3;
-      const int per_tile = kTile / a.page_size;
+      const int per_tile = kTile >> a.page_shift;
       const uint32_t page_bytes = static_cast<uint32_t>(a.page_size) * D * 2;
       const uint32_t stages = is_v ? VS : KS, data = is_v ? sV : sK;
       const uint32_t full0 = is_v ? BAR_VF(0) : BAR_KF(0), bars = is_v ? VB : KB, empty0 = is_v ? BAR_VE(0) : BAR_KE(0);
@@ -1481,11 +1487,13 @@ ta_status launch_decode_shared(const void* q, const void* k_cache, const void* v
   a.group_offsets = group_offsets;
   a.prefix_lens = prefix_lens;
   a.page_size = page_size;
+  while (1 << a.page_shift < page_size) ++a.page_shift;
   a.num_seqs = num_seqs;
   a.num_groups = num_groups;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.G = Hq / Hkv;
+  while (1 << a.g_shift < a.G) ++a.g_shift;
   a.max_pages = max_pages;
   a.num_pages_total = num_pages_total;
   a.n_ctas = plan.n_ctas;
