@@ -412,7 +412,9 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
  * rows themselves are used by every sequence of the group.  Out-of-range
  * lengths, prefix lengths and table entries are clamped on the device and
  * flagged; offsets that decrease or leave the batch are flagged and no prefix
- * is shared.  The result does not depend on scheduling.
+ * is shared.  The result does not depend on scheduling.  A score that is NaN
+ * or +inf makes its row NaN, in o and lse, and no other; one of -inf weighs
+ * nothing, and a row of which all are -inf gets O = 0, lse = -inf.
  */
 size_t attn_paged_decode_shared_workspace_size(int num_seqs, int num_groups, int Hq, int Hkv, int d);
 ta_status attn_paged_decode_shared(const void *q, const void *k_cache, const void *v_cache,

@@ -1098,11 +1098,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kG; ++i)
           if (i < G) {
-            const float inv = l[i] > 0.f ? __fdividef(1.f, l[i]) : 0.f;
+            // no weight at all (every score -inf): an empty partial; a NaN sum (a score NaN or +inf) goes on to the join
+            const float inv = l[i] == 0.f ? 0.f : __fdividef(1.f, l[i]);
             if (lane_row < D) a.own_o[(at + i) * D + lane_row] = __uint_as_float(orr[i]) * inv;
             if (lane_row == i && sg.tiles == 1) a.own_lse[(at ^ G) + i] = -INFINITY;   // the unit's other partial is none
             if (lane_row == i)
-              a.own_lse[at + i] = l[i] > 0.f ? fmaf(m[i], a.scale, __log2f(l[i]) * 0.69314718055994531f) : -INFINITY;
+              a.own_lse[at + i] = l[i] == 0.f ? -INFINITY : fmaf(m[i], a.scale, __log2f(l[i]) * 0.69314718055994531f);
           }
         continue;
       }
@@ -1199,11 +1200,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- the partial: O / l and m scale + ln l, in fp32
+      // ---- the partial: O / l and m scale + ln l, in fp32; NaN where l is (own keys do the same)
       if (!(ok = product_done(1))) break;
       if (warp_live) {
         const size_t slot = static_cast<size_t>(sg.slot);
-        const float inv = (l > 0.f) ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         // [slot][4 columns][256 rows]: a warp's rows side by side
         float4* dst = reinterpret_cast<float4*>(a.pre_o) + slot * (D / 4) * kUnitRows + half * kTile + row;
 #pragma unroll 1
@@ -1223,7 +1224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!sg.wide && sg.tiles == 1)   // the unit's other partial is none
             a.pre_lse[slot * kUnitRows + (half ^ 1) * kTile + row] = -INFINITY;
           a.pre_lse[slot * kUnitRows + half * kTile + row] =
-              (l > 0.f) ? fmaf(m, a.scale, __log2f(l) * 0.69314718055994531f) : -INFINITY;
+              l == 0.f ? -INFINITY : fmaf(m, a.scale, __log2f(l) * 0.69314718055994531f);
         }
       }
       tc_fence_before();
@@ -1321,15 +1322,15 @@ __global__ void __launch_bounds__(G * D / 4 * kLanes) shared_combine_kernel(cons
     float mn = m;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, w[k]);
-    if (mn == -INFINITY) continue;
-    const float s0 = __expf(m - mn);
+    const float top = mn == -INFINITY ? 0.f : mn;   // the max passes over a NaN, whose weight must not be lost
+    const float s0 = __expf(m - top);
     m = mn;
     l *= s0;
     acc = make_float4(acc.x * s0, acc.y * s0, acc.z * s0, acc.w * s0);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
       if (w[k] != -INFINITY) {   // an empty partial's values may be anything
-        const float s1 = __expf(w[k] - mn);
+        const float s1 = __expf(w[k] - top);
         l += s1;
         acc.x = fmaf(s1, v[k].x, acc.x);
         acc.y = fmaf(s1, v[k].y, acc.y);
@@ -1357,13 +1358,13 @@ __global__ void __launch_bounds__(G * D / 4 * kLanes) shared_combine_kernel(cons
     if (threadIdx.x == 0) *a.status = bits;
   }
   if (lane0 != 0) return;
-  const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+  const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);   // NaN stays
   const size_t orow = static_cast<size_t>(seq) * a.Hq + hkv * G + gq;
   uint2 w2;
   w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(o + orow * D)[c4] = w2;
-  if (c4 == 0 && lse) lse[orow] = l > 0.f ? m + __logf(l) : -INFINITY;
+  if (c4 == 0 && lse) lse[orow] = l == 0.f ? -INFINITY : m + __logf(l);
 }
 
 // ---------------------------------------------------------------------------
