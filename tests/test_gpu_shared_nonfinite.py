@@ -1,7 +1,8 @@
 """Scores that are not finite in the shared-prefix decode: a NaN or +inf score
 makes its row NaN (output and lse), as softmax of it is; a score of -inf is a
 weight of 0; every other row keeps its bits.  A row all of whose scores are
--inf is one without visible keys: O = 0, lse = -inf.
+-inf is one without visible keys: O = 0, lse = -inf.  And scores near the ends
+of fp32's range under a scale that brings them back.
 
 Error bound of the finite rows that meet a -inf score: that of
 test_gpu_shared.py, over the keys whose scores are finite.
@@ -169,3 +170,18 @@ def test_all_scores_minus_infinity(cuda):
         want = expect(torch, b)
         assert bool(torch.isnan(want[2]).any()) and bool(torch.isneginf(want[2]).any())
         compare(torch, b.run(torch, binding), want, clean, touched, "all keys")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,ps", [(8, 2, 128, 16), (8, 1, 64, 8)])
+def test_small_scales_and_large_scores(cuda, Hq, Hkv, d, ps):
+    # the scale may be far below the smallest difference of scores: 0 weighs all keys alike however large they are,
+    # and a tiny one is applied as it is
+    torch, binding = cuda
+    b = Batch(torch, [(300, [40, 2, 90]), (None, [33])], Hq, Hkv, d, ps, seed=d + 1)
+    b.q, b.k = b.q * 2.0 ** 50, b.k * 2.0 ** 50
+    for scale in (0.0, d ** -0.5 * 2.0 ** -100, d ** -0.5 * 2.0 ** -103):
+        want = expect(torch, b, scale)
+        assert bool(torch.isfinite(want[2]).all())
+        nothing = torch.ones(b.S, Hq, dtype=torch.bool)
+        got = b.run(torch, binding, scale)
+        compare(torch, got, want, got, nothing, f"scale {scale}")

@@ -1500,9 +1500,9 @@ ta_status launch_decode_shared(const void* q, const void* k_cache, const void* v
   a.n_ctas = plan.n_ctas;
   a.max_own = max_own_len;
   a.scale = scale;
-  // a scale of 0 (equal weights) becomes one so small that finite scores still weigh 1: masked scores are -inf, and
-  // 0 times that would be NaN
-  a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1e-30f);
+  // a scale of 0 (equal weights) becomes the smallest number there is, 2^-149: masked scores are -inf, and 0 times
+  // that would be NaN; finite ones come to less than 2^-21 and weigh 1
+  a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1.4e-45f);
   a.status = reinterpret_cast<unsigned*>(ws);
   a.per_cta = reinterpret_cast<long long*>(ws + 128);
   a.cta_status = reinterpret_cast<unsigned*>(ws + plan.cta_status);
