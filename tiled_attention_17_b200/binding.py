@@ -425,8 +425,8 @@ def _scope(device, stream):
     import contextlib
     import torch
     if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+        if isinstance(stream, int):   # 0 is the default stream's handle (an ExternalStream of 0 is one of torch's pool)
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     stack = contextlib.ExitStack()
