@@ -246,12 +246,15 @@ ta_status attn_rope(const void *x, void *y, const int32_t *positions, const doub
  * cu_seqlens[num_seqs] on) write nothing, in q_out as well, and no slot but
  * the new tokens' is written.  Lengths and offsets out of range (a sequence
  * shorter than its new tokens, longer than max_pages * page_size, offsets that
- * decrease or pass `total`) and table entries outside the pool are flagged in
- * the library status word (ta_device_status): a token with a bad length or
- * offset writes nothing, one with a bad page writes its q_out row only.  Two
- * tokens whose table entries name the same slot race.  Supported: d in {64,
- * 128}, page_size in {8, 16, 32, 64}, rotary_dim a multiple of 16 in [0, d],
- * Hq + 2 Hkv <= 65535, max_pages * page_size <= 2^30, total <= 2^30.
+ * decrease or leave [0, total]) and table entries outside the pool are flagged
+ * in the library status word (ta_device_status): offsets wherever they stand,
+ * the others where a token meets them.  A sequence with a bad length or bad
+ * offsets brings nothing; a token with a bad page writes its q_out row only.
+ * Where offsets decrease a row may lie in two sequences' ranges: it is then
+ * written for one of them at most.  Two tokens whose table entries name the
+ * same slot race.  total == 0 or num_seqs == 0 does nothing.  Supported: d in
+ * {64, 128}, page_size in {8, 16, 32, 64}, rotary_dim a multiple of 16 in
+ * [0, d], Hq + 2 Hkv <= 65535, max_pages * page_size <= 2^30, total <= 2^30.
  * Allocates nothing.
  */
 ta_status attn_paged_append(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
