@@ -247,9 +247,10 @@ ta_status attn_rope(const void *x, void *y, const int32_t *positions, const doub
  * the new tokens' is written.  Lengths and offsets out of range (a sequence
  * shorter than its new tokens, longer than max_pages * page_size, offsets that
  * decrease or leave [0, total]) and table entries outside the pool are flagged
- * in the library status word (ta_device_status): offsets wherever they stand,
- * the others where a token meets them.  A sequence with a bad length or bad
- * offsets brings nothing; a token with a bad page writes its q_out row only.
+ * in the library status word (ta_device_status): lengths and offsets of every
+ * sequence, with or without new tokens, table entries where a token meets
+ * them.  A sequence with a bad length or bad offsets brings nothing; a token
+ * with a bad page writes its q_out row only.
  * Where offsets decrease a row may lie in two sequences' ranges: it is then
  * written for one of them at most.  Two tokens whose table entries name the
  * same slot race.  total == 0 or num_seqs == 0 does nothing.  Supported: d in

@@ -92,3 +92,19 @@ def test_a_sequence_past_the_rows_leaves_the_others_alone(cuda):
     b, inv, got = append(torch, binding, [0, 1, 2, 30], [9, 4, 60], 3)
     assert got[3] == binding.TA_DEV_BAD_SEQ_LEN
     check_batch(torch, b, got, b.expect(torch, inv, 1.0, False, skip={2}))
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 20, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("where", [0, 1, 3])
+def test_bad_lengths_of_sequences_without_tokens_are_flagged(cuda, bad, where):
+    torch, binding = cuda
+    cu, lens = [0, 0, 0, 3, 3], [4, 8, 9, 2]
+    b = Batch(torch, [0, 0, 3, 0], lens, 2, 1, 64, 8, 64, seed=7)
+    inv, _ = freqs(torch, 64)
+    seq_lens = b.seq_lens.clone()
+    seq_lens[where] = bad
+    got = b.run(torch, binding, inv, seq_lens=seq_lens)
+    assert got[3] == binding.TA_DEV_BAD_SEQ_LEN
+    check_batch(torch, b, got, b.expect(torch, inv, 1.0, False))
+    got = b.run(torch, binding, inv)
+    assert got[3] == 0

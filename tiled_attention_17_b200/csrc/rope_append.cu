@@ -221,13 +221,14 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
     stride = (a.num_seqs + kMaxStaged - 1) / kMaxStaged;
     staged = a.num_seqs / stride;   // samples: the ends of sequences stride - 1, 2 stride - 1, ...
     for (int i = threadIdx.x; i < staged; i += kRopeThreads) s_cu[i] = __ldg(a.cu_seqlens + (i + 1) * stride);
-    // Every sequence's offsets are looked at, by one block or another: no token need lead to a bad one.
+    // Every sequence's offsets and length are looked at, by one block or another: no token need lead to a bad one.
     if (blockIdx.y == 0) {
       unsigned bad = 0;
       for (int64_t s = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x; s < a.num_seqs;
            s += static_cast<int64_t>(gridDim.x) * kRopeThreads) {
-        const int first = __ldg(a.cu_seqlens + s), end = __ldg(a.cu_seqlens + s + 1);
-        if (first < 0 || end < first || end > a.total) bad = kDevBadSeqLen;
+        const int first = __ldg(a.cu_seqlens + s), end = __ldg(a.cu_seqlens + s + 1), len = __ldg(a.seq_lens + s);
+        if (first < 0 || end < first || end > a.total || len < end - first || len > a.max_pages * a.page_size)
+          bad = kDevBadSeqLen;
       }
       if (bad) atomicOr(a.status, bad);
     }
