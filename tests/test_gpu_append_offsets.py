@@ -108,3 +108,23 @@ def test_bad_lengths_of_sequences_without_tokens_are_flagged(cuda, bad, where):
     check_batch(torch, b, got, b.expect(torch, inv, 1.0, False))
     got = b.run(torch, binding, inv)
     assert got[3] == 0
+
+
+@pytest.mark.parametrize("s", [0, 12345, 18943, 18944, 19999])
+def test_more_sequences_than_one_round_of_blocks_looks_at(cuda, s):
+    # 148 blocks of 128 threads take a sequence each at a time
+    torch, binding = cuda
+    S = 20000
+    cu, lens = [0] * (S + 1), [1] * S
+    for bad in (False, True):
+        if bad:
+            lens[s] = -1
+        table = torch.zeros(S, 1, dtype=torch.int32, device="cuda")
+        kc, vc = (torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        k = torch.ones(3, 1, 64, dtype=torch.bfloat16, device="cuda")
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+        binding.ta_device_status(True)
+        binding.paged_append(k, k, kc, vc, table, i32(lens), i32(cu))
+        torch.cuda.synchronize()
+        assert binding.ta_device_status(True) == (0, binding.TA_DEV_BAD_SEQ_LEN if bad else 0)
+        assert not bool(kc.any()) and not bool(vc.any())

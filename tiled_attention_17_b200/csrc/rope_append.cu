@@ -168,6 +168,7 @@ struct AppendArgs {
   int64_t qt, qh, kt, kh, vt, vh;   // strides in elements
   int page_size, num_seqs, total, Hq, Hkv, max_pages, num_pages_total, rotary_dim;
   int heads;                        // rows one thread walks over
+  int token_blocks;                 // blocks (in x) of tokens; those behind look at the sequences
   float amp;
   unsigned* status;
 };
@@ -187,6 +188,19 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
   __shared__ Place s_place[kTokens];
   const int u = threadIdx.x % kUnits, in_block = threadIdx.x / kUnits;
   const int t0 = blockIdx.x * kTokens, tok = t0 + in_block;
+  if (static_cast<int>(blockIdx.x) >= a.token_blocks) {
+    // The blocks behind the tokens' look at every sequence's offsets and length: no token need lead to a bad one.  (In
+    // the tokens' blocks the same loop took registers from their loads: 4 long prompts 131 -> 140 us.)
+    unsigned bad = 0;
+    for (int64_t s = static_cast<int64_t>(blockIdx.x - a.token_blocks) * kRopeThreads + threadIdx.x;
+         s < a.num_seqs && blockIdx.y == 0; s += static_cast<int64_t>(gridDim.x - a.token_blocks) * kRopeThreads) {
+      const int first = __ldg(a.cu_seqlens + s), end = __ldg(a.cu_seqlens + s + 1), len = __ldg(a.seq_lens + s);
+      if (first < 0 || end < first || end > a.total || len < end - first || len > a.max_pages * a.page_size)
+        bad = kDevBadSeqLen;
+    }
+    if (bad) atomicOr(a.status, bad);
+    return;
+  }
   bool turns;
   int va, vb;
   unit_vectors<kPairs>(u, a.rotary_dim, turns, va, vb);
@@ -221,17 +235,6 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
     stride = (a.num_seqs + kMaxStaged - 1) / kMaxStaged;
     staged = a.num_seqs / stride;   // samples: the ends of sequences stride - 1, 2 stride - 1, ...
     for (int i = threadIdx.x; i < staged; i += kRopeThreads) s_cu[i] = __ldg(a.cu_seqlens + (i + 1) * stride);
-    // Every sequence's offsets and length are looked at, by one block or another: no token need lead to a bad one.
-    if (blockIdx.y == 0) {
-      unsigned bad = 0;
-      for (int64_t s = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x; s < a.num_seqs;
-           s += static_cast<int64_t>(gridDim.x) * kRopeThreads) {
-        const int first = __ldg(a.cu_seqlens + s), end = __ldg(a.cu_seqlens + s + 1), len = __ldg(a.seq_lens + s);
-        if (first < 0 || end < first || end > a.total || len < end - first || len > a.max_pages * a.page_size)
-          bad = kDevBadSeqLen;
-      }
-      if (bad) atomicOr(a.status, bad);
-    }
     __syncthreads();
   }
   if (threadIdx.x < kTokens) {
@@ -406,8 +409,13 @@ ta_status launch_paged_append(const void* q, const void* k, const void* v, void*
   const int units = d / 16, per_block = kRopeThreads / units;
   const int rows = (q ? Hq : 0) + 2 * Hkv;
   a.heads = heads_per_thread(static_cast<int64_t>(total) * units, rows);
-  const dim3 grid(static_cast<unsigned>((total + per_block - 1) / per_block),
-                  static_cast<unsigned>((rows + a.heads - 1) / a.heads));
+  a.token_blocks = (total + per_block - 1) / per_block;
+  int seq_blocks = 0;
+  if (cu_seqlens) {   // with one token each the tokens are the sequences
+    seq_blocks = (num_seqs - 1) / kRopeThreads + 1;
+    if (seq_blocks > 148) seq_blocks = 148;
+  }
+  const dim3 grid(static_cast<unsigned>(a.token_blocks + seq_blocks), static_cast<unsigned>((rows + a.heads - 1) / a.heads));
   if (d == 128) {
     if (interleaved) paged_append_kernel<128, true><<<grid, kRopeThreads, 0, stream>>>(a);
     else paged_append_kernel<128, false><<<grid, kRopeThreads, 0, stream>>>(a);
