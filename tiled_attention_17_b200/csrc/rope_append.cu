@@ -15,14 +15,13 @@
 // approximation: within 2^-21 of 1, next to the 2^-8 a bf16 result is rounded by.
 //
 // Bound: HBM bytes, each element read once and written once.  One thread owns
-// 16 elements (8 pairs) of a row and walks over heads of its token with the
-// eight cosines and sines in registers, so the trigonometry is paid once per
-// token and not once per head; two 16-byte loads per head, four heads in
-// flight before the first is used.  How many heads a thread walks over is
-// chosen in heads_per_thread (below).  Measured (B200): 4 x 4096 tokens, 16 heads
-// of 128 in 24 us (5.6 TB/s), 16686 tokens of 48 rows of 128 appended in 69 us (5.9
-// TB/s), one token in 3.4 us.  With 2 or 8 heads in flight, blocks of 256, or
-// loads marked as streaming the appends take 2 to 20% longer.
+// 16 elements (8 pairs) of a row, in up to four heads of its token: the eight
+// cosines and sines are formed once for them, while their loads (two of 16 bytes a
+// head) are all in flight.  How many heads a thread takes is chosen in
+// heads_per_thread (below).  Measured (B200): 4 x 4096 tokens, 16 heads of 128 in
+// 24 us (5.6 TB/s), 16686 tokens of 48 rows of 128 appended in 69 us (5.9 TB/s), one
+// token in 3.4 us.  With 2 or 8 heads in flight, blocks of 256, or loads marked as
+// streaming the appends take 2 to 20% longer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +34,7 @@ namespace ta {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kInFlight = 4;      // heads loaded before the first is used
+constexpr int kMaxHeads = 4;   // heads one thread takes at most, all loaded before the first is used
 
 // Eight cosines and sines of pairs [8 u, 8 u + 8) at one position.
 struct Turn {
@@ -104,7 +103,7 @@ struct RopeArgs {
   const double* inv_freq;
   int64_t xb, xh, xn, yb, yh, yn, pb;   // strides in elements
   int64_t tokens;                       // B * N
-  int N, H, rotary_dim, heads;          // heads: heads one thread walks over
+  int N, H, rotary_dim, heads;          // heads: heads one thread takes
   float amp, sign;
 };
 
@@ -122,30 +121,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   const __nv_bfloat16* src = a.x + b * a.xb + n * a.xn;
   __nv_bfloat16* dst = a.y + b * a.yb + n * a.yn;
 
-  uint4 ra[kInFlight], rb[kInFlight];
-  auto load = [&](int h) {
+  uint4 ra[kMaxHeads], rb[kMaxHeads];   // in flight while the angles are formed
 #pragma unroll
-    for (int j = 0; j < kInFlight; ++j)
-      if (h + j < h1) {
-        const uint4* row = reinterpret_cast<const uint4*>(src + (h + j) * a.xh);
-        ra[j] = row[va];
-        rb[j] = row[vb];
-      }
-  };
-  load(h0);   // in flight while the angles are formed
+  for (int j = 0; j < kMaxHeads; ++j)
+    if (h0 + j < h1) {
+      const uint4* row = reinterpret_cast<const uint4*>(src + (h0 + j) * a.xh);
+      ra[j] = row[va];
+      rb[j] = row[vb];
+    }
   Turn t;
   if (turns) make_turn(t, a.positions ? __ldg(a.positions + b * a.pb + n) : static_cast<int>(n), a.inv_freq, u, a.amp, a.sign);
-  for (int h = h0; h < h1; h += kInFlight) {
 #pragma unroll
-    for (int j = 0; j < kInFlight; ++j)
-      if (h + j < h1) {
-        if (turns) turn_row<kPairs>(ra[j], rb[j], t);
-        uint4* row = reinterpret_cast<uint4*>(dst + (h + j) * a.yh);
-        row[va] = ra[j];
-        row[vb] = rb[j];
-      }
-    load(h + kInFlight);
-  }
+  for (int j = 0; j < kMaxHeads; ++j)
+    if (h0 + j < h1) {
+      if (turns) turn_row<kPairs>(ra[j], rb[j], t);
+      uint4* row = reinterpret_cast<uint4*>(dst + (h0 + j) * a.yh);
+      row[va] = ra[j];
+      row[vb] = rb[j];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -167,7 +160,7 @@ struct AppendArgs {
   const double* inv_freq;
   int64_t qt, qh, kt, kh, vt, vh;   // strides in elements
   int page_size, num_seqs, total, Hq, Hkv, max_pages, num_pages_total, rotary_dim;
-  int heads;                        // rows one thread walks over
+  int heads;                        // rows one thread takes
   int token_blocks;                 // blocks (in x) of tokens; those behind look at the sequences
   float amp;
   unsigned* status;
@@ -209,21 +202,18 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
   const int h0 = blockIdx.y * a.heads, h1 = min(rows, h0 + a.heads);
   const bool in = tok < a.total;
 
-  uint4 ra[kInFlight], rb[kInFlight];
-  auto load = [&](int h) {
+  uint4 ra[kMaxHeads], rb[kMaxHeads];   // in flight while the tokens' places are found
 #pragma unroll
-    for (int j = 0; j < kInFlight; ++j)
-      if (in && h + j < h1) {
-        const int r = h + j;
-        const __nv_bfloat16* p = r < hq            ? a.q + tok * a.qt + r * a.qh
-                                 : r < hq + a.Hkv ? a.k + tok * a.kt + (r - hq) * a.kh
-                                                  : a.v + tok * a.vt + (r - hq - a.Hkv) * a.vh;
-        const uint4* row = reinterpret_cast<const uint4*>(p);
-        ra[j] = row[va];
-        rb[j] = row[vb];
-      }
-  };
-  load(h0);   // in flight while the tokens' places are found
+  for (int j = 0; j < kMaxHeads; ++j)
+    if (in && h0 + j < h1) {
+      const int r = h0 + j;
+      const __nv_bfloat16* p = r < hq            ? a.q + tok * a.qt + r * a.qh
+                               : r < hq + a.Hkv ? a.k + tok * a.kt + (r - hq) * a.kh
+                                                : a.v + tok * a.vt + (r - hq - a.Hkv) * a.vh;
+      const uint4* row = reinterpret_cast<const uint4*>(p);
+      ra[j] = row[va];
+      rb[j] = row[vb];
+    }
 
   // The sequence of a token: the number of sequence ends at or before it,
   // found by bisection among the ends staged in shared memory (every end up to
@@ -300,28 +290,25 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
   Turn t;
   if (turns && h0 < hq + a.Hkv) make_turn(t, pl.pos, a.inv_freq, u, a.amp, 1.f);
   const int64_t page_row = (static_cast<int64_t>(pl.page) * a.Hkv * a.page_size + pl.row) * D;
-  for (int h = h0; h < h1; h += kInFlight) {
 #pragma unroll
-    for (int j = 0; j < kInFlight; ++j)
-      if (h + j < h1) {
-        const int r = h + j;
-        const bool is_q = r < hq, is_v = r >= hq + a.Hkv;
-        if (turns && !is_v) turn_row<kPairs>(ra[j], rb[j], t);
-        if (is_q || pl.page >= 0) {
-          const int64_t head = static_cast<int64_t>(is_v ? r - hq - a.Hkv : r - hq) * a.page_size * D;
-          __nv_bfloat16* p = is_q   ? a.q_out + (static_cast<int64_t>(tok) * a.Hq + r) * D
-                             : is_v ? a.v_cache + page_row + head
-                                    : a.k_cache + page_row + head;
-          uint4* row = reinterpret_cast<uint4*>(p);
-          row[va] = ra[j];
-          row[vb] = rb[j];
-        }
+  for (int j = 0; j < kMaxHeads; ++j)
+    if (h0 + j < h1) {
+      const int r = h0 + j;
+      const bool is_q = r < hq, is_v = r >= hq + a.Hkv;
+      if (turns && !is_v) turn_row<kPairs>(ra[j], rb[j], t);
+      if (is_q || pl.page >= 0) {
+        const int64_t head = static_cast<int64_t>(is_v ? r - hq - a.Hkv : r - hq) * a.page_size * D;
+        __nv_bfloat16* p = is_q   ? a.q_out + (static_cast<int64_t>(tok) * a.Hq + r) * D
+                           : is_v ? a.v_cache + page_row + head
+                                  : a.k_cache + page_row + head;
+        uint4* row = reinterpret_cast<uint4*>(p);
+        row[va] = ra[j];
+        row[vb] = rb[j];
       }
-    load(h + kInFlight);
-  }
+    }
 }
 
-// Heads one thread walks over.  More heads share one token's angles (about as much
+// Heads one thread takes.  More heads share one token's angles (about as much
 // work as three heads), fewer give more threads.  Measured on a B200 (us, 1 / 2 /
 // 4 / 8 heads): forward of 4 x 4096 tokens, 16 + 16 heads of 128: 97 / 61 / 48 / 49;
 // ragged append of 16686 tokens, 48 rows: 167 / 98 / 72 / 76; 3 x 1021 tokens, 6 + 2
@@ -330,7 +317,7 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const Append
 // to a full machine, else four.
 int heads_per_thread(int64_t threads_per_head, int heads) {
   const int64_t threads = threads_per_head * heads;
-  const int per = threads <= 148 * 4 * 64 ? 1 : threads <= 148 * 1024 / 2 ? 2 : 4;
+  const int per = threads <= 148 * 4 * 64 ? 1 : threads <= 148 * 1024 / 2 ? 2 : kMaxHeads;
   return per < heads ? per : heads;
 }
 
