@@ -121,3 +121,30 @@ def test_banded_scalings_keep_fast_pairs_and_divide_slow_ones(kind):
 def test_frequency_refusals(args):
     with pytest.raises(ValueError):
         rope.frequency_list(*args)
+
+
+def test_yarn_ramp_at_known_pairs():
+    # trained 4096, base 10^4, 64 pairs: 32 turns fall at pair 64 ln(4096 / 64 pi) / ln 10^4 = 20.94, one turn at
+    # 64 ln(4096 / 2 pi) / ln 10^4 = 45.03, so the ramp goes from pair 20 to pair 46
+    f, _ = rope.frequency_list(128)
+    g, _ = rope.frequency_list(128, scaling={"type": "yarn", "factor": 16.0, "trained_length": 4096})
+    for pair, kept in ((0, 1.0), (20, 1.0), (21, 25 / 26), (26, 20 / 26), (33, 0.5), (45, 1 / 26), (46, 0.0), (63, 0.0)):
+        assert g[pair] == pytest.approx(f[pair] * (kept + (1 - kept) / 16), rel=1e-12), pair
+    # other betas: 16 turns at 25.76, 2 turns at 40.21
+    g, _ = rope.frequency_list(128, scaling={"type": "yarn", "factor": 4.0, "trained_length": 4096, "beta_fast": 16.0,
+                                             "beta_slow": 2.0})
+    for pair, kept in ((25, 1.0), (33, 0.5), (37, 0.25), (41, 0.0)):
+        assert g[pair] == pytest.approx(f[pair] * (kept + (1 - kept) / 4), rel=1e-12), pair
+
+
+@pytest.mark.parametrize("turns,kept", [(0.5, 0.0), (1.0, 0.0), (1.75, 0.25), (2.5, 0.5), (3.25, 0.75), (4.0, 1.0), (9.0, 1.0)])
+def test_wavelength_ramp_at_known_turns(turns, kept):
+    # pair 1 of 4 at base 10^4 turns by 0.1 a position: `turns` over this trained length; the ramp is linear in the turns
+    trained = turns * 2 * math.pi / 0.1
+    g, amp = rope.frequency_list(8, 10000.0, {"type": "wavelength", "factor": 8.0, "trained_length": trained})
+    assert amp == 1.0 and g[1] == pytest.approx(0.1 * (kept + (1 - kept) / 8), rel=1e-12)
+    # other ends of the ramp
+    g, _ = rope.frequency_list(8, 10000.0, {"type": "wavelength", "factor": 8.0, "trained_length": trained, "low_turns": 0.5,
+                                            "high_turns": 8.5})
+    share = min(max((turns - 0.5) / 8, 0.0), 1.0)
+    assert g[1] == pytest.approx(0.1 * (share + (1 - share) / 8), rel=1e-12)

@@ -15,9 +15,11 @@ Scalings (a context `factor` times the trained one):
                length are kept, those that turn less than beta_slow times are
                divided by the factor, a linear ramp over the pair index
                between; amplitude 0.1 ln(factor) + 1 (Peng et al. 2023)
-  wavelength   the same idea with the ramp over the number of turns: pairs with
-               more than high_turns turns over the trained length are kept,
-               those with fewer than low_turns are divided by the factor
+  wavelength   the same with the ramp over the number of turns itself: a pair
+               of t turns over the trained length (the length divided by the
+               pair's wavelength) keeps (t - low_turns) / (high_turns -
+               low_turns) of its frequency, within [0, 1], the rest is divided
+               by the factor; amplitude 1 ("by parts" in Peng et al. 2023)
 """
 from __future__ import annotations
 
