@@ -190,7 +190,8 @@ ta_status attn_lse_merge_finish(const float *acc_o, void *out, int64_t rows, int
  *     a' = amplitude (a cos t - b sin t),  b' = amplitude (a sin t + b cos t)
  * and elements from rotary_dim on are copied.  inverse = 1 turns by -t: with
  * the same amplitude that is the gradient of the forward call (the transposed
- * map).  Angles are formed in fp64 and each result is rounded once.
+ * map).  Angles are formed in fp64, their sines and cosines are within 2^-21,
+ * and each result is rounded to bf16 once.
  *
  *   x, y         bf16 [B, H, N, d] with the strides given (in elements, for
  *                batch, head and token; the d elements of a row are
@@ -408,7 +409,10 @@ ta_status attn_paged_decode_noalloc(const void *q, const void *k_cache, const vo
  *                with the device current that the call will run on: partials
  *                are kept for each of its SMs), 256-byte aligned; the status
  *                word is read by attn_paged_decode_check.  Must not be shared
- *                by calls that may run concurrently
+ *                by calls that may run concurrently.  Partials of 256 rows (d *
+ *                1 KB) are kept for each group and KV head however few
+ *                sequences it has: 729 MiB, 594 of them for prefixes, for 512
+ *                groups of 8 sequences with 32 + 8 heads of 128
  *
  * Supported: the shapes of attn_paged_decode, max_pages * page_size <= 2^30,
  * num_groups <= 65535, num_pages_total * Hkv < 2^31.  Pool rows behind a

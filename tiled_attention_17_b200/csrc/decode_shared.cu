@@ -18,7 +18,8 @@
 // Measured (B200, whole call, L2 cold): 64 sequences, 32 + 8 heads of 128, 8000
 // shared and up to 512 own tokens 42 us (the bytes alone 15); 96 sequences in 6
 // groups, 32 + 4 heads of 64, 5000 shared and up to 1024 own tokens 45 us (12);
-// 256 sequences behind 30000 tokens 162 us, 190 in a long run (products 77).  The time
+// 256 sequences behind 30000 tokens 162 us, 188 in a long run, whose power holds the
+// SM clock at 1.64 GHz instead of 1.97 (products 77).  The time
 // goes to the start (6 us: plan, tensor memory, first tiles), the steps, and the
 // join (7 us).  A step with two row tiles, 128 keys, takes 3800 cycles, of which
 // tensor pipe 2600 (products of 64 keys are bound by the reads of Q from shared
@@ -57,14 +58,21 @@ constexpr int kThreads = 416;
 constexpr int kSoftmaxWarp0 = 4, kMmaWarp1 = 12;
 constexpr float kRescaleLog2 = 8.0f;   // the stale-max margin of the prefill kernel
 // Cost of a step with two row tiles, and with one.  Measured 2.33 us (256 samples
-// behind 30000 shared tokens: both tiles' softmax) and 1.36 us (their own tokens,
-// segments of one or two steps: latency); at 2 : 1 the last CTA ended 17% after
-// the median.
+// behind 30000 shared tokens: both tiles' softmax; 3800 cycles at the 1.64 GHz of a
+// long run) and 1.36 us (their own tokens, segments of one or two steps: latency);
+// at 2 : 1 the last CTA ended 17% after the median.  All of these are of d = 128 and 4
+// heads a group, and are used for every layout: at d = 64 a wide step has half the
+// products and the same exponentials, and its own costs were not measured.
 // A further unit with wide steps costs a CTA some 4 us more than the steps (its
 // partial is 128 KB, and the pipeline starts again): without a cost of its own the
 // CTAs with two of them ended 25% after the median of a small batch.
 constexpr int kWideCost = 5, kNarrowCost = 3, kWideStart = 8;
-constexpr int kApart = 1000;   // cycles between the row tiles' first softmax of a wide segment
+// Cycles between the row tiles' first softmax of a wide segment (why: where it is waited).  With and without, us a call
+// of a long run: d = 128, 4 heads a group, 6 groups of 64 sequences behind 4000 tokens 80.1 / 85.0, 64 behind 8000 43.4 /
+// 43.7, 256 behind 30000 183.0 / 183.6; d = 64, 8 heads, within 0.3% (96 behind 5000 32.9 / 32.9, 256 behind 20000 133.0 /
+// 132.5, 40 groups of 32 behind 1000 123.9 / 123.8), and so are segments of a single wide step (20 groups of 64 behind 112
+// tokens, d = 128, 144.3 / 144.3).
+constexpr int kApart = 1000;
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -736,8 +744,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tS = tbase + (t ? L::kTmS1 : L::kTmS0), tO = tbase + (t ? L::kTmO1 : L::kTmO0);
       constexpr bool kTwo = L::kChunks == 2;
       constexpr uint64_t kTileStep = L::kTileBytes >> 4;
-      // (made from the tile's address: adding t tiles to a descriptor, with t the same in all lanes, came out of the
-      // compiler with a wrong upper half, and every row but a tile's first was wrong)
       const uint64_t dQ = smem_desc_sw128(sQ + (t ? L::kTileBytes : 0), 16, 1024);
       const uint64_t dK = smem_desc_sw128(sK, 16, L::kChunks * 1024);   // 8-row groups hold every chunk
       const int ps = a.page_size;
@@ -1061,7 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_st();
             }
           }
-          // weights into P^T [query][key], 128-byte rows of 64 keys, 16-byte pieces swizzled by the row
+          // weights into P^T [query][key], 128-byte rows of 64 keys, 16-byte pieces swizzled by the row; rounded to bf16,
+          // the type of V, as the prefix's are (below); the sum is of the unrounded ones
           uint8_t* const pk = prow + (own_k & 1u) * kOwnPBytes + pbyte;
           auto weigh = [&](int i) {
             const float negm = (m[i] == -INFINITY) ? 0.f : -m[i] * c2;
@@ -1119,8 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           // Two row tiles in step form their exponentials at the same time (985 cycles for 64 of them, twice one warp's
           // time) and leave the unit idle at the same time.  Nothing moves them apart, so tile 1 starts a segment a
-          // quarter of a step late: 256 samples behind 30000 tokens 164 -> 162 us, 64 behind 8000 tokens 45.0 -> 43.7
-          // (700 cycles: 167 and 43.7).
+          // quarter of a step (of d = 128) late: figures at kApart.
           if (t == 1 && first && sg.wide)
             for (const long long t0 = clock64(); clock64() - t0 < kApart;) {
             }
@@ -1177,7 +1183,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // Weights 2^((s - m) c2), packed to bf16 for the tensor product (the rounding
-          // of the prefill kernels; the sum is of the unrounded values).  c2 > 0 (see
+          // of the prefill kernels: the operands of one product have one type, and V is
+          // bf16.  An output is 0.0023 off, relative, where its own rounding alone makes
+          // 0.0017; the sum is of the unrounded values).  c2 > 0 (see
           // the host side), so masked columns are exactly 0.  The weights take the
           // columns of their scores.
           const float negm = (m == -INFINITY) ? 0.f : -m * c2;
